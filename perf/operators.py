@@ -231,7 +231,7 @@ def prepare(case, seed):
         s["scale"] = scale.squeeze(-1).contiguous()
         if own:
             from sparse_gemm_amd import patch
-            s["weight"] = patch.W4Weight(s["q"], s["scale"], s["zero"], gr)
+            s["weight"] = patch.w4_pack(s["q"], s["scale"], s["zero"], gr)
     return s
 
 
