@@ -410,6 +410,235 @@ patch_status patch_gemm_noalloc(const patch_packed_desc* desc, const void* packe
                                 void* Y_dev, patch_dtype y_dtype, void* stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * The operators of a decoder layer that run next to its projections: rotary
+ * positions, the append of new keys and values to a paged 8-bit cache,
+ * attention over that cache, and a linear layer with 4-bit weights.
+ *
+ * Their arguments come in structures of 8-byte fields (strides in elements;
+ * the last index of every tensor is contiguous).  Data that a captured graph
+ * changes between replays -- positions, lengths, page numbers -- is device
+ * memory the host never reads, so the kernels check it: what each does with
+ * a value out of range is stated below.  All calls are asynchronous on
+ * `stream`; T == 0 or S == 0 is a no-op.
+ * ---------------------------------------------------------------------------
+ *
+ * Rotary positions.  The first `rot` elements of a head are rot/2 pairs; pair
+ * i of a token at position p turns by the angle p * f_i:
+ *   (a, b) -> (a cos - b sin, b cos + a sin),
+ * the pair being elements (i, i + rot/2) (PATCH_ROPE_HALF) or (2i, 2i + 1)
+ * (PATCH_ROPE_INTERLEAVED); elements from `rot` on stay as they are.
+ *
+ * patch_rope_table fills table_dev, float32 [positions][rot]: row p holds
+ * m cos(p f_i) for i < rot/2, then m sin(p f_i), computed in 64 bits and
+ * rounded once.  f_i = base^(-2i/rot), scaled for contexts longer than the
+ * `original` one by `scaling`:
+ *   PATCH_ROPE_UNSCALED   f_i
+ *   PATCH_ROPE_LINEAR     f_i / factor (positions interpolated)
+ *   PATCH_ROPE_NTK        base replaced by base * factor^(rot / (rot - 2))
+ *                         (rot >= 4): the slowest pair interpolated, the
+ *                         fastest untouched
+ *   PATCH_ROPE_BY_PARTS   g f_i + (1 - g) f_i / factor, g = (r - low) / (high
+ *                         - low) clamped to [0, 1], r = original f_i / (2 pi)
+ *                         the pair's turns over the original context
+ * `magnitude` (m) multiplies cos and sin (1 for a pure rotation).
+ * Errors: PATCH_ERR_SHAPE (positions < 1, rot odd or < 2, over 2^31 entries
+ * a row count), PATCH_ERR_INVALID_ARG (null or unaligned table, unknown
+ * scaling, base <= 1, factor < 1, magnitude, original, low or high out of
+ * range or not finite).
+ */
+typedef enum { PATCH_ROPE_HALF = 0, PATCH_ROPE_INTERLEAVED = 1 } patch_rope_layout;
+typedef enum {
+  PATCH_ROPE_UNSCALED = 0,
+  PATCH_ROPE_LINEAR = 1,
+  PATCH_ROPE_NTK = 2,
+  PATCH_ROPE_BY_PARTS = 3
+} patch_rope_scaling;
+
+patch_status patch_rope_table(int64_t positions, int64_t rot, double base, int32_t scaling, double factor,
+                              double original, double low, double high, double magnitude, float* table_dev,
+                              void* stream);
+
+/*
+ * patch_rope: out = x turned by each token's position; `inverse` turns by
+ * the negative angle, which (times the table's magnitude) is the transposed
+ * map: the gradient of x from the gradient of out.  x and out are T x H x D
+ * of `dtype` (PATCH_F16, PATCH_BF16 or PATCH_F32) with the strides given;
+ * out may be x itself with x's strides, and must not overlap it otherwise.
+ * The arithmetic is fp32, rounded once.  positions: int32 [T]; a position
+ * outside 0 .. context - 1 (context: the table's rows) makes the token's
+ * rotated elements NaN.
+ * Errors: PATCH_ERR_SHAPE (D or rot odd or < 2, rot > D, H < 1, sizes beyond
+ * 2^31 items), PATCH_ERR_INVALID_ARG (null pointers, pointers not aligned to
+ * their element, dtype, layout, context < 1, T < 0).
+ */
+typedef struct {
+  int64_t dtype, layout, inverse;
+  int64_t T, H, D, rot, context;
+  const void* x_dev;
+  int64_t x_token, x_head;
+  void* out_dev;
+  int64_t out_token, out_head;
+  const int32_t* positions_dev;
+  const float* table_dev;
+} patch_rope_args;
+patch_status patch_rope(const patch_rope_args* args, void* stream);
+
+/*
+ * The paged 8-bit cache.  k and v hold `pages` blocks of `page` tokens for
+ * each of kv_heads heads: [pages][kv_heads][page][dim] e4m3 values (one sign,
+ * four exponent, three fraction bits, no infinities), contiguous; k_scale and
+ * v_scale, float32 [pages][kv_heads], are what a block's values stand to be
+ * multiplied by.  page is 16, 32, 64 or 128; dim a multiple of 16 up to 256.
+ * A sequence's tokens t sit in page page_table[s][t / page], place t % page.
+ */
+typedef struct {
+  void* k_dev;
+  void* v_dev;
+  float* k_scale_dev;
+  float* v_scale_dev;
+  int64_t pages, kv_heads, page, dim;
+} patch_kv_cache;
+
+/*
+ * patch_kv_append: the tokens cu_new[s] .. cu_new[s+1] - 1 of k, v and q are
+ * the newest of sequence s, whose length with them is kv_lens[s]; they take
+ * the places kv_lens[s] - n .. kv_lens[s] - 1 and those positions.  k and q
+ * are rotated as patch_rope does (table NULL: not), v is not.  Per block and
+ * head that receives tokens:
+ *   scale = 2^ceil(log2(amax / 448)), at least 2^-126, amax the largest finite
+ *           |value| received (after rotation, fp32); where the block already
+ *           holds tokens of the sequence (places before the first new one),
+ *           at least its present scale, and if the scale grows the held values
+ *           are rounded again to it,
+ *   value = round to nearest even e4m3 of x * (1 / scale); NaN and infinite x
+ *           are stored as NaN.
+ * Powers of two lose nothing beside the 8-bit rounding itself.  q_out = q
+ * rotated, rounded to dtype (q NULL: none; q_out may be q).  Places that no
+ * new token takes, and rows of k, v, q behind cu_new[S], are left as they
+ * are.  Every (block, head) belongs to one workgroup or part of one: no
+ * atomics, same results every time.
+ *
+ *   k_dev, v_dev   T x kv_heads x dim of dtype (PATCH_F16, PATCH_BF16)
+ *   q_dev          T x heads x dim
+ *   page_table     int32 [S][max_pages], rows page_table_row apart
+ *   kv_lens        int32 [S];  cu_new  int32 [S + 1], not decreasing, from 0
+ *   table          float32 [context][rot] of patch_rope_table, or NULL
+ * A page that receives tokens must belong to one sequence alone.  New tokens
+ * whose place is negative, behind max_pages, or in a page outside 0 ..
+ * pages - 1 are not stored; positions outside the table make the rotated
+ * elements NaN (q) or stored as NaN (k); tokens outside 0 .. T - 1 are not
+ * read.
+ * Errors: PATCH_ERR_SHAPE (sizes as above, rot odd, < 2 or > dim),
+ * PATCH_ERR_INVALID_ARG (null pointers, misalignment, dtype, layout).
+ */
+typedef struct {
+  int64_t dtype, layout;
+  int64_t T, S, heads, rot, context, max_pages;
+  const void* k_dev;
+  int64_t k_token, k_head;
+  const void* v_dev;
+  int64_t v_token, v_head;
+  const void* q_dev;
+  int64_t q_token, q_head;
+  void* q_out_dev;
+  int64_t q_out_token, q_out_head;
+  const int32_t* page_table_dev;
+  int64_t page_table_row;
+  const int32_t* kv_lens_dev;
+  const int32_t* cu_new_dev;
+  const float* table_dev;
+} patch_kv_append_args;
+patch_status patch_kv_append(const patch_kv_append_args* args, const patch_kv_cache* cache, void* stream);
+
+/*
+ * patch_attention: out = softmax(scale q k^T) v over the cache, for the
+ * newest n = cu_new[s+1] - cu_new[s] tokens of every sequence (appended
+ * before): token i of them sits at position p = kv_lens[s] - n + i and sees
+ * the keys 0 .. p, with window > 0 only the last `window` of them.  Query
+ * head h reads cache head h / (heads / kv_heads).  q: T x heads x dim of
+ * `dtype` (PATCH_F16, PATCH_BF16); out: T x heads x dim of out_dtype (dtype
+ * or PATCH_F32); lse (may be NULL): float32 [T][heads], the natural logarithm
+ * of the softmax's sum.  Products run on the 16-bit matrix instructions (8-bit
+ * values are exact in them), the probabilities rounded to 11 bits for the
+ * second product; scores, maxima, sums and outputs are fp32, the outputs
+ * rounded once.
+ *   A token that sees no key (negative position): out 0, lse -infinity.  A
+ * page number outside 0 .. pages - 1 among the pages it sees, or a length
+ * beyond max_pages * page: out and lse NaN.  Keys, values and scales that a
+ * token does not see do not reach its output, NaN among them.  Scales must
+ * be finite.  Rows of out and lse behind cu_new[S] are left as they are.
+ *   workspace: patch_attention_workspace_bytes(...) bytes of scratch, 16-byte
+ * aligned, contents of no matter before and after; calls that may run at the
+ * same time need workspaces of their own.  NULL or a smaller one: no work is
+ * split, same results but for rounding.
+ * Errors: PATCH_ERR_SHAPE (cache sizes, heads no multiple of kv_heads, S over
+ * 4096), PATCH_ERR_INVALID_ARG (null pointers, misalignment, dtypes, scale not
+ * finite, window < 0).
+ */
+typedef struct {
+  int64_t dtype, out_dtype;
+  int64_t T, S, heads, max_pages, window;
+  double scale;
+  const void* q_dev;
+  int64_t q_token, q_head;
+  void* out_dev;
+  int64_t out_token, out_head;
+  float* lse_dev;
+  const int32_t* page_table_dev;
+  int64_t page_table_row;
+  const int32_t* kv_lens_dev;
+  const int32_t* cu_new_dev;
+} patch_attention_args;
+uint64_t patch_attention_workspace_bytes(int64_t T, int64_t S, int64_t heads, int64_t kv_heads, int64_t dim);
+patch_status patch_attention(const patch_attention_args* args, const patch_kv_cache* cache, void* workspace_dev,
+                             uint64_t workspace_bytes, void* stream);
+
+/*
+ * Linear layer with 4-bit weights and group scales, for the few tokens of a
+ * decode step: Y = X W^T, W[n][k] = (q[n][k] - zero[n][k / group]) *
+ * scale[n][k / group], q in 0 .. 15, group 32, 64 or 128, N any size from 1,
+ * K a multiple of group.
+ *
+ * patch_w4_quantize rounds a weight to that form: per group, with zero_dev
+ * NULL scale = amax / 7 rounded to dtype, q = round(w / scale) + 8 clamped to
+ * 1 .. 15 (the zero is 8 throughout); else lo = min(0, smallest), hi = max(0,
+ * largest), scale = (hi - lo) / 15 rounded to dtype, zero = round(-lo / scale)
+ * and q = round(w / scale) + zero, each clamped to 0 .. 15.  Rounding is to
+ * nearest even in fp32; where the scale rounds to 0 it is 0, zero and q being
+ * 8 (zero_dev: 0).  Weights must be finite.
+ *
+ *   q      uint8 [N][K / 2], column 2i in the low half of byte i
+ *   scale  dtype [N][K / group];  zero  uint8 [N][K / group] in 0 .. 15 (only
+ *          the low four bits are read), or NULL: 8 everywhere
+ *
+ * patch_w4_pack lays them out for the product, patch_w4_bytes(...) bytes in
+ * packed_dev: per band of 16 rows, first the weights of 128 columns at a time
+ * (1 KB: lane l's 16 bytes at 16 l, row l % 16; its 32-bit word j holds the
+ * columns 32 j + 8 (l / 16) .. + 7, column 2i in bits 4i.., 2i + 1 in bits 16
+ * + 4i..), K padded to 128; after all bands the scales, per band [group][16
+ * rows] of dtype, then with zero the zeros likewise, a byte each.  Rows behind
+ * N and columns behind K: zeros.
+ *
+ * patch_w4_gemm: X M x K of dtype (PATCH_F16, PATCH_BF16), Y M x N of y_dtype
+ * (dtype or PATCH_F32), both contiguous.  Weights are exact in the matrix
+ * instructions; sums are fp32, a group's sum multiplied by its scale in fp32.
+ * Any M >= 0 runs; the weights are read once for every 64 rows of X, so many
+ * tokens are better served by the GEMMs above.
+ * Errors: PATCH_ERR_SHAPE (sizes), PATCH_ERR_INVALID_ARG (null pointers,
+ * misalignment, dtypes, M < 0), PATCH_ERR_BUFFER_TOO_SMALL (packed).
+ */
+uint64_t patch_w4_bytes(int64_t N, int64_t K, int64_t group, int32_t with_zero);
+patch_status patch_w4_quantize(patch_dtype dtype, int64_t N, int64_t K, int64_t group, const void* W_dev,
+                               uint8_t* q_dev, void* scale_dev, uint8_t* zero_dev, void* stream);
+patch_status patch_w4_pack(patch_dtype dtype, int64_t N, int64_t K, int64_t group, const uint8_t* q_dev,
+                           const void* scale_dev, const uint8_t* zero_dev, void* packed_dev, uint64_t packed_bytes,
+                           void* stream);
+patch_status patch_w4_gemm(patch_dtype dtype, int64_t N, int64_t K, int64_t group, int32_t with_zero,
+                           const void* packed_dev, uint64_t packed_bytes, const void* X_dev, int64_t M, void* Y_dev,
+                           patch_dtype y_dtype, void* stream);
+
+/*
  * For tests of the prefill kernel's bounded wait.  In the tail split (the
  * output blocks left over after whole rounds of the GPU, cut into K ranges
  * that hand their fp32 sums to the block's first range through the

@@ -1,0 +1,301 @@
+// gemm_w4.hip -- linear layer with 4-bit weights and group scales, for few
+// tokens: Y = X W^T, W = (q - z) s per group of columns.
+//
+// Decode reads every weight once, so the product is bound by the N K / 2
+// bytes of the weights (plus scales); the matrix cores do the arithmetic, 16
+// columns of which only the M tokens count.  W is the A operand of
+// v_mfma_f32_16x16x32 (16 rows of W), X the B operand (16 tokens).
+//
+//   * Weights become 16-bit values by OR alone: 16 + q has q in the top four
+//     fraction bits of 16.0 (fp16 0x4c00 | q << 6, bf16 0x4180 | q << 3), so a
+//     shift and a v_and_or_b32 make two operand elements.
+//   * The 16 + z too much is taken off per group: sum x (16 + q) - (16 + z) sum
+//     x, the second sum by the same instruction with an A operand of ones --
+//     both exact products added in fp32 -- and the difference is multiplied by
+//     the group's scale in fp32.  16 is the smallest such offset, so the
+//     cancellation costs three bits of an fp32 sum at most.
+//   * A band's weights lie in lane order (patch_w4_pack), 1 KB for 128 columns:
+//     one 16-byte load a lane feeds four matrix instructions.
+//   * A workgroup has one band of 16 rows; its waves take the 128-column blocks
+//     in turn and join their sums through LDS in a fixed order.
+#include <algorithm>
+
+#include "device_common.h"
+#include "layer_common.h"
+
+namespace patch {
+namespace {
+
+constexpr int kWaves = 8;
+
+// The eight operand elements 16 + q of a packed word.
+template <bool BF16>
+__device__ __forceinline__ u32x4 widen4(uint32_t w) {
+  u32x4 r;
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    if constexpr (BF16) {
+      const uint32_t b = i == 0 ? w << 3 : w >> (4 * i - 3);
+      r[i] = (b & 0x00780078u) | 0x41804180u;
+    } else {
+      const uint32_t b = i < 2 ? w << (6 - 4 * i) : w >> (4 * i - 6);
+      r[i] = (b & 0x03c003c0u) | 0x4c004c00u;
+    }
+  }
+  return r;
+}
+
+struct W4Args {
+  const uint8_t* w;      // bands of blocks
+  const uint8_t* scale;  // [band][group][16] 16-bit
+  const uint8_t* zero;   // [band][group][16] bytes
+  const void* X;
+  void* Y;
+  int64_t M, N, K;
+  int blocks;  // 128-column blocks of a band
+  int groups;  // groups of a row
+};
+
+// MT blocks of 16 tokens, G columns a group.
+template <bool BF16, bool OUT_F32, int MT, int G, bool ZERO>
+__global__ __launch_bounds__(kWaves * 64) void k_w4(W4Args a) {
+  __shared__ f32x4 part[kWaves][MT][64];
+  const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6, n = lane & 15, g = lane >> 4;
+  const int64_t band = blockIdx.x, m0 = (int64_t)blockIdx.y * (16 * MT);
+  const uint8_t* wp = a.w + (band * a.blocks) * 1024 + lane * 16;
+  const uint8_t* sp = a.scale + (band * a.groups * 16 + 4 * g) * 2;
+  const uint8_t* zp = ZERO ? a.zero + band * a.groups * 16 + 4 * g : nullptr;
+  const uint16_t* xp[MT];
+#pragma unroll
+  for (int t = 0; t < MT; t++)
+    xp[t] = reinterpret_cast<const uint16_t*>(a.X) + std::min(m0 + 16 * t + n, a.M - 1) * a.K;  // rows behind M: the last, not stored
+  const uint32_t one2 = BF16 ? 0x3f803f80u : 0x3c003c00u;
+  const u32x4 ones = {one2, one2, one2, one2};
+  constexpr int kGroups = 128 / G;  // groups of a block
+  constexpr int kJ = G / 32;        // instructions of a group
+  f32x4 y[MT];
+#pragma unroll
+  for (int t = 0; t < MT; t++) y[t] = (f32x4){0.f, 0.f, 0.f, 0.f};
+
+  for (int b = wave; b < a.blocks; b += kWaves) {
+    const u32x4 w = ld16(wp + (int64_t)b * 1024);
+    u32x4 x[MT][4];
+#pragma unroll
+    for (int t = 0; t < MT; t++)
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        const int64_t k = (int64_t)b * 128 + 32 * j + 8 * g;
+        x[t][j] = ld16_pred(xp[t] + k, k < a.K);  // columns behind K are zeros in X too
+      }
+#pragma unroll
+    for (int q = 0; q < kGroups; q++) {
+      const int gr = b * kGroups + q;
+      if (gr >= a.groups) break;
+      const u32x2 s2 = *reinterpret_cast<const u32x2*>(sp + (int64_t)gr * 32);
+      float s[4], z[4];
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        const uint16_t h = (uint16_t)(s2[i >> 1] >> (16 * (i & 1)));
+        s[i] = BF16 ? __uint_as_float((uint32_t)h << 16) : (float)__builtin_bit_cast(_Float16, h);
+      }
+      if constexpr (ZERO) {
+        const uint32_t zw = *reinterpret_cast<const uint32_t*>(zp + (int64_t)gr * 16);
+#pragma unroll
+        for (int i = 0; i < 4; i++) z[i] = 16.0f + (float)((zw >> (8 * i)) & 15u);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; i++) z[i] = 24.0f;
+      }
+      u32x4 wq[kJ];
+#pragma unroll
+      for (int j = 0; j < kJ; j++) wq[j] = widen4<BF16>(w[q * kJ + j]);
+#pragma unroll
+      for (int t = 0; t < MT; t++) {
+        f32x4 acc = {0.f, 0.f, 0.f, 0.f}, sum = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < kJ; j++) {
+          acc = mma_dense<BF16>(wq[j], x[t][q * kJ + j], acc);
+          sum = mma_dense<BF16>(ones, x[t][q * kJ + j], sum);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; i++) y[t][i] += s[i] * (acc[i] - z[i] * sum[i]);
+      }
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < MT; t++) part[wave][t][lane] = y[t];
+  __syncthreads();
+  // lane l of block t holds rows 4 (l / 16) .. + 3, token l % 16
+  for (int e = (int)threadIdx.x; e < MT * 64; e += kWaves * 64) {
+    const int t = e >> 6, l = e & 63;
+    f32x4 v = part[0][t][l];
+#pragma unroll
+    for (int w = 1; w < kWaves; w++) v += part[w][t][l];
+    const int64_t m = m0 + 16 * t + (l & 15), row = band * 16 + 4 * (l >> 4);
+    if (m >= a.M || row >= a.N) continue;
+    if (row + 4 <= a.N && (a.N & 3) == 0) {
+      store4<BF16, OUT_F32>(a.Y, m * a.N + row, v);
+    } else {
+      for (int i = 0; i < 4 && row + i < a.N; i++) {
+        if constexpr (OUT_F32)
+          reinterpret_cast<float*>(a.Y)[m * a.N + row + i] = v[i];
+        else if constexpr (BF16)
+          reinterpret_cast<__bf16*>(a.Y)[m * a.N + row + i] = (__bf16)v[i];
+        else
+          reinterpret_cast<_Float16*>(a.Y)[m * a.N + row + i] = (_Float16)v[i];
+      }
+    }
+  }
+}
+
+// ---- layout ----
+__host__ __device__ inline int64_t n_bands(int64_t N) { return (N + 15) / 16; }
+__host__ __device__ inline int64_t n_blocks(int64_t K) { return (K + 127) / 128; }
+inline int64_t scale_offset(int64_t N, int64_t K) { return n_bands(N) * n_blocks(K) * 1024; }
+inline int64_t zero_offset(int64_t N, int64_t K, int64_t G) { return scale_offset(N, K) + n_bands(N) * 16 * (K / G) * 2; }
+
+// One thread a 32-bit word of the weights, then one a scale and zero.
+__global__ __launch_bounds__(256) void k_w4_pack(int64_t N, int64_t K, int64_t G, const uint8_t* __restrict__ q,
+                                                 const uint16_t* __restrict__ scale, const uint8_t* __restrict__ zero,
+                                                 uint32_t* __restrict__ w, uint16_t* __restrict__ so,
+                                                 uint8_t* __restrict__ zo) {
+  const int64_t words = n_bands(N) * n_blocks(K) * 256, groups = K / G, extra = n_bands(N) * groups * 16;
+  for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < words + extra; e += (int64_t)gridDim.x * 256) {
+    if (e < words) {
+      const int64_t block = e >> 8, band = block / n_blocks(K);
+      const int j = (int)e & 3, l = (int)(e >> 2) & 63;
+      const int64_t row = band * 16 + (l & 15), k = (block - band * n_blocks(K)) * 128 + 32 * j + 8 * (l >> 4);
+      uint32_t v = 0;
+      if (row < N && k < K) {  // K and k are multiples of 8
+        const uint32_t b = *reinterpret_cast<const uint32_t*>(q + row * (K / 2) + k / 2);
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+          v |= ((b >> (8 * i)) & 15u) << (4 * i) | ((b >> (8 * i + 4)) & 15u) << (16 + 4 * i);
+      }
+      w[e] = v;
+    } else {
+      const int64_t f = e - words, band = f / (groups * 16), r = f - band * groups * 16, gr = r >> 4, row = band * 16 + (r & 15);
+      so[f] = row < N ? scale[row * groups + gr] : (uint16_t)0;
+      if (zo) zo[f] = row < N ? zero[row * groups + gr] & 15 : 0;
+    }
+  }
+}
+
+// One wave a group at a time: G = 32, 64 or 128 columns, two neighbours a lane.
+template <typename T>
+__global__ __launch_bounds__(256) void k_w4_quantize(int64_t N, int64_t K, int G, const T* __restrict__ W,
+                                                     uint8_t* __restrict__ q, T* __restrict__ scale,
+                                                     uint8_t* __restrict__ zero) {
+  const int lane = (int)threadIdx.x & 63, per = 128 / G, sub = lane / (G / 2);  // groups of a wave
+  const int64_t groups = K / G, all = N * groups;
+  for (int64_t g0 = ((int64_t)blockIdx.x * 4 + (threadIdx.x >> 6)) * per; g0 < all; g0 += (int64_t)gridDim.x * 4 * per) {
+    const int64_t gi = g0 + sub;
+    const bool ok = gi < all;
+    const int64_t at = gi * G + 2 * (lane % (G / 2));  // rows are whole groups: element index = group index * G + column
+    const float x = ok ? (float)W[at] : 0.f, y = ok ? (float)W[at + 1] : 0.f;
+    float hi = fmaxf(x, y), lo = fminf(x, y);
+    for (int d = 1; d < G / 2; d *= 2) {
+      hi = fmaxf(hi, __shfl_xor(hi, d));
+      lo = fminf(lo, __shfl_xor(lo, d));
+    }
+    T st;
+    float z = 8.0f;
+    float s;
+    if (zero) {
+      hi = fmaxf(hi, 0.f);
+      lo = fminf(lo, 0.f);
+      st = (T)((hi - lo) / 15.0f);
+      s = (float)st;
+      z = s > 0.f ? fminf(15.f, fmaxf(0.f, rintf(-lo / s))) : 8.f;
+    } else {
+      st = (T)(fmaxf(hi, -lo) / 7.0f);
+      s = (float)st;
+    }
+    const float least = zero ? 0.f : 1.f;
+    const float qx = s > 0.f ? fminf(15.f, fmaxf(least, rintf(x / s) + z)) : 8.f;
+    const float qy = s > 0.f ? fminf(15.f, fmaxf(least, rintf(y / s) + z)) : 8.f;
+    if (ok) {
+      q[at / 2] = (uint8_t)((uint32_t)qx | (uint32_t)qy << 4);
+      if (lane % (G / 2) == 0) {
+        scale[gi] = st;
+        if (zero) zero[gi] = (uint8_t)z;
+      }
+    }
+  }
+}
+
+template <bool BF16, bool OUT_F32, int MT, int G, bool ZERO>
+hipError_t go(const W4Args& a, hipStream_t s) {
+  const int64_t my = (a.M + 16 * MT - 1) / (16 * MT);
+  if (my > 65535) return hipErrorInvalidValue;
+  hipLaunchKernelGGL((k_w4<BF16, OUT_F32, MT, G, ZERO>), dim3((unsigned)n_bands(a.N), (unsigned)my), dim3(kWaves * 64), 0,
+                     s, a);
+  return hipGetLastError();
+}
+template <bool BF16, bool OUT_F32, int MT, int G>
+hipError_t by_zero(const W4Args& a, hipStream_t s) {
+  return a.zero ? go<BF16, OUT_F32, MT, G, true>(a, s) : go<BF16, OUT_F32, MT, G, false>(a, s);
+}
+template <bool BF16, bool OUT_F32, int MT>
+hipError_t by_group(const W4Args& a, hipStream_t s) {
+  switch (a.K / a.groups) {
+    case 32: return by_zero<BF16, OUT_F32, MT, 32>(a, s);
+    case 64: return by_zero<BF16, OUT_F32, MT, 64>(a, s);
+    default: return by_zero<BF16, OUT_F32, MT, 128>(a, s);
+  }
+}
+template <bool BF16, bool OUT_F32>
+hipError_t by_tokens(const W4Args& a, hipStream_t s) {
+  if (a.M <= 16) return by_group<BF16, OUT_F32, 1>(a, s);
+  if (a.M <= 32) return by_group<BF16, OUT_F32, 2>(a, s);
+  return by_group<BF16, OUT_F32, 4>(a, s);
+}
+
+}  // namespace
+
+uint64_t w4_bytes(int64_t N, int64_t K, int64_t G, bool zero) {
+  return (uint64_t)(zero_offset(N, K, G) + (zero ? n_bands(N) * 16 * (K / G) : 0));
+}
+
+hipError_t launch_w4_quantize(bool bf16, int64_t N, int64_t K, int group, const void* W, uint8_t* q, void* scale,
+                              uint8_t* zero, hipStream_t s) {
+  const int64_t waves = (N * (K / group) + 128 / group - 1) / (128 / group);
+  const unsigned blocks = (unsigned)std::min<int64_t>((waves + 3) / 4, 65536);
+  if (bf16)
+    hipLaunchKernelGGL((k_w4_quantize<__bf16>), dim3(blocks), dim3(256), 0, s, N, K, group,
+                       reinterpret_cast<const __bf16*>(W), q, reinterpret_cast<__bf16*>(scale), zero);
+  else
+    hipLaunchKernelGGL((k_w4_quantize<_Float16>), dim3(blocks), dim3(256), 0, s, N, K, group,
+                       reinterpret_cast<const _Float16*>(W), q, reinterpret_cast<_Float16*>(scale), zero);
+  return hipGetLastError();
+}
+
+hipError_t launch_w4_pack(int64_t N, int64_t K, int group, const uint8_t* q, const void* scale, const uint8_t* zero,
+                          uint8_t* packed, hipStream_t s) {
+  const int64_t all = n_bands(N) * n_blocks(K) * 256 + n_bands(N) * 16 * (K / group);
+  const unsigned blocks = (unsigned)std::min<int64_t>((all + 255) / 256, 65536);
+  hipLaunchKernelGGL(k_w4_pack, dim3(blocks), dim3(256), 0, s, N, K, (int64_t)group, q,
+                     reinterpret_cast<const uint16_t*>(scale), zero, reinterpret_cast<uint32_t*>(packed),
+                     reinterpret_cast<uint16_t*>(packed + scale_offset(N, K)),
+                     zero ? packed + zero_offset(N, K, group) : nullptr);
+  return hipGetLastError();
+}
+
+hipError_t launch_w4_gemm(bool bf16, bool out_f32, bool zero, int64_t N, int64_t K, int group, const uint8_t* packed,
+                          const void* X, int64_t M, void* Y, hipStream_t s) {
+  W4Args a;
+  a.w = packed;
+  a.scale = packed + scale_offset(N, K);
+  a.zero = zero ? packed + zero_offset(N, K, group) : nullptr;
+  a.X = X;
+  a.Y = Y;
+  a.M = M;
+  a.N = N;
+  a.K = K;
+  a.blocks = (int)n_blocks(K);
+  a.groups = (int)(K / group);
+  if (bf16) return out_f32 ? by_tokens<true, true>(a, s) : by_tokens<true, false>(a, s);
+  return out_f32 ? by_tokens<false, true>(a, s) : by_tokens<false, false>(a, s);
+}
+
+}  // namespace patch

@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import dataclasses
 import os
+import struct
 from typing import Optional
 
 import numpy as np
@@ -53,8 +54,9 @@ EXPORTS = ("patch_abi_version", "patch_packed_bytes", "patch_pack", "patch_packe
            "patch_dense_gemm_swiglu", "patch_packed_bytes_concat", "patch_pack_concat", "patch_sample_mask",
            "patch_exec_tile_map", "patch_apply_fine_mask", "patch_probe_stream_read", "patch_probe_matrix_rate", "patch_probe_copy_rate", "patch_probe_copy_bytes",
            "patch_debug_tail_wait",
-           "patch_probe_matrix_flops", "patch_noalloc_scratch_bytes", "patch_gemm_noalloc", "patch_status_string",
-           "patch_last_error")
+           "patch_probe_matrix_flops", "patch_noalloc_scratch_bytes", "patch_gemm_noalloc", "patch_rope_table",
+           "patch_rope", "patch_kv_append", "patch_attention_workspace_bytes", "patch_attention", "patch_w4_bytes",
+           "patch_w4_quantize", "patch_w4_pack", "patch_w4_gemm", "patch_status_string", "patch_last_error")
 
 _lib = None
 
@@ -131,6 +133,25 @@ def load():
     lib.patch_noalloc_scratch_bytes.restype = U64
     lib.patch_gemm_noalloc.argtypes = [DP, P, P, I64, P, ctypes.c_int, P]
     lib.patch_gemm_noalloc.restype = ctypes.c_int
+    F64 = ctypes.c_double
+    lib.patch_rope_table.argtypes = [I64, I64, F64, I32, F64, F64, F64, F64, F64, P, P]
+    lib.patch_rope_table.restype = ctypes.c_int
+    lib.patch_rope.argtypes = [P, P]
+    lib.patch_rope.restype = ctypes.c_int
+    lib.patch_kv_append.argtypes = [P, P, P]
+    lib.patch_kv_append.restype = ctypes.c_int
+    lib.patch_attention_workspace_bytes.argtypes = [I64, I64, I64, I64, I64]
+    lib.patch_attention_workspace_bytes.restype = U64
+    lib.patch_attention.argtypes = [P, P, P, U64, P]
+    lib.patch_attention.restype = ctypes.c_int
+    lib.patch_w4_bytes.argtypes = [I64, I64, I64, I32]
+    lib.patch_w4_bytes.restype = U64
+    lib.patch_w4_quantize.argtypes = [ctypes.c_int, I64, I64, I64, P, P, P, P, P]
+    lib.patch_w4_quantize.restype = ctypes.c_int
+    lib.patch_w4_pack.argtypes = [ctypes.c_int, I64, I64, I64, P, P, P, P, U64, P]
+    lib.patch_w4_pack.restype = ctypes.c_int
+    lib.patch_w4_gemm.argtypes = [ctypes.c_int, I64, I64, I64, I32, P, U64, P, I64, P, ctypes.c_int, P]
+    lib.patch_w4_gemm.restype = ctypes.c_int
     lib.patch_status_string.argtypes = [ctypes.c_int]
     lib.patch_status_string.restype = ctypes.c_char_p
     lib.patch_last_error.argtypes = []
@@ -629,3 +650,320 @@ def probe_copy_rate(src: torch.Tensor, window_bytes: int, iters: int, workgroups
     _check(lib.patch_probe_copy_rate(_ptr(src), src.numel() * src.element_size(), window_bytes, iters, workgroups,
                                      _ptr(sink), sink.numel() * sink.element_size(), _stream(src.device.index)))
     return int(lib.patch_probe_copy_bytes(iters, workgroups))
+
+
+# ---------------------------------------------------------------------------- decoder-layer operators
+# Their C structures are 8-byte fields in order: packed here with struct.
+_ROPE_ARGS = struct.Struct("16q")
+_APPEND_ARGS = struct.Struct("25q")
+_ATTENTION_ARGS = struct.Struct("7qd11q")
+_CACHE_ARGS = struct.Struct("8q")
+_LAYOUTS = {"half": 0, "interleaved": 1}
+_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "by_parts": 3}
+
+
+class _Device:
+    """Makes a tensor's device the current one for a call, where it is not:
+    a launch goes to the current device."""
+
+    def __init__(self, index: int):
+        self.index = index
+
+    def __enter__(self):
+        self.before = torch.cuda.current_device()
+        if self.before != self.index:
+            torch.cuda.set_device(self.index)
+
+    def __exit__(self, *exc):
+        if self.before != self.index:
+            torch.cuda.set_device(self.before)
+
+
+def _call(device: torch.device, fn, *args):
+    """A library call on the device's current stream."""
+    i = device.index
+    if torch.cuda.current_device() == i:
+        rc = fn(*args, _stream(i))
+    else:
+        with _Device(i):
+            rc = fn(*args, _stream(i))
+    if rc != 0:
+        _check(rc)
+
+
+def _heads(t, name: str, dtype, shape):
+    """A [tokens, heads, dim] tensor whose elements of a head are contiguous;
+    returns its address and the other two strides.  A size of None is free."""
+    _need(isinstance(t, torch.Tensor), f"{name} must be a torch tensor")
+    _need(t.dtype == dtype, f"{name} must be {dtype}, not {t.dtype}")
+    _need(t.dim() == 3, f"{name} must have three dimensions (tokens, heads, dim), not {t.dim()}")
+    s = t.shape
+    _need(s[0] == shape[0] and (shape[1] is None or s[1] == shape[1]) and (shape[2] is None or s[2] == shape[2]),
+          f"{name} must have shape {tuple(shape)}, not {tuple(s)}")
+    st = t.stride()
+    _need(st[2] == 1 or s[2] == 1, f"{name}: the elements of a head must be contiguous")
+    return t.data_ptr(), st[0], st[1]
+
+
+def _index(t, name: str, n: int):
+    _need(isinstance(t, torch.Tensor), f"{name} must be a torch tensor")
+    _need(t.dtype == torch.int32 and t.dim() == 1 and t.shape[0] == n and (n < 2 or t.stride(0) == 1),
+          f"{name} must be a contiguous int32 tensor of {n}")
+    return t.data_ptr()
+
+
+def _on_device(device, *named):
+    _need(device.type == "cuda", "tensors must be on the device")
+    for name, t in named:
+        if t is not None:
+            _need(t.device == device, f"{name} must be on {device}, not {t.device}")
+
+
+def rope_table(positions: int, rot: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+               original: float = 0.0, low: float = 1.0, high: float = 32.0, magnitude: float = 1.0, device="cuda",
+               out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """cos and sin of every position's angles, float32 [positions, rot]
+    (patch_rope_table).  scaling: "none", "linear", "ntk" or "by_parts", for
+    contexts `factor` times the `original` one."""
+    lib = _lib or load()
+    _need(scaling in _SCALINGS, f"scaling must be one of {sorted(_SCALINGS)}, not {scaling!r}")
+    _check_out(out, (positions, rot), torch.float32)
+    if out is None:
+        _need(positions >= 1 and rot >= 2, f"positions={positions} and rot={rot} must be positive")
+        out = torch.empty((positions, rot), dtype=torch.float32, device=device)
+    _on_device(out.device)
+    _call(out.device, lib.patch_rope_table, positions, rot, base, _SCALINGS[scaling], factor, original, low, high,
+          magnitude, out.data_ptr())
+    return out
+
+
+def _table_of(table: Optional[torch.Tensor]):
+    if table is None:
+        return 0, 0, 0
+    _need(isinstance(table, torch.Tensor) and table.dtype == torch.float32 and table.dim() == 2
+          and table.is_contiguous(), "table must be a contiguous float32 tensor (positions, rot)")
+    return table.data_ptr(), table.shape[0], table.shape[1]
+
+
+def rope(x: torch.Tensor, positions: torch.Tensor, table: torch.Tensor, layout: str = "half", inverse: bool = False,
+         out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """x [tokens, heads, dim] (float16, bfloat16 or float32; any token and
+    head stride) turned by each token's position, int32 [tokens]
+    (patch_rope).  inverse=True turns back: the gradient of x from that of
+    the result.  out may be x."""
+    lib = _lib or load()
+    _need(layout in _LAYOUTS, f"layout must be one of {sorted(_LAYOUTS)}, not {layout!r}")
+    _need(isinstance(x, torch.Tensor) and x.dim() == 3, "x must be a 3-D tensor (tokens, heads, dim)")
+    _need(x.dtype in _TORCH_DT, f"unsupported dtype {x.dtype}")
+    T, H, D = x.shape
+    xp, xt, xh = _heads(x, "x", x.dtype, (T, H, D))
+    pos = _index(positions, "positions", T)
+    _need(table is not None, "table must be a tensor")
+    tp, context, rot = _table_of(table)
+    _on_device(x.device, ("positions", positions), ("table", table), ("out", out))
+    if out is None:
+        out = torch.empty((T, H, D), dtype=x.dtype, device=x.device)
+    op, ot, oh = _heads(out, "out", x.dtype, (T, H, D))
+    _call(x.device, lib.patch_rope,
+          _ROPE_ARGS.pack(_TORCH_DT[x.dtype], _LAYOUTS[layout], bool(inverse), T, H, D, rot, context, xp, xt, xh, op, ot,
+                          oh, pos, tp))
+    return out
+
+
+@dataclasses.dataclass(frozen=True)
+class KVCache:
+    """The pages of a paged 8-bit cache (patch_kv_cache): k, v [pages,
+    kv_heads, page, dim] of torch.float8_e4m3fn (or uint8 bits), k_scale,
+    v_scale float32 [pages, kv_heads]; all contiguous on one device.  Checked
+    here once; the tensors stay the caller's."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: torch.Tensor
+    v_scale: torch.Tensor
+
+    def __post_init__(self):
+        k = self.k
+        _need(isinstance(k, torch.Tensor) and k.dim() == 4, "k must be a 4-D tensor (pages, kv_heads, page, dim)")
+        _need(k.dtype in (torch.float8_e4m3fn, torch.uint8), "k must be float8_e4m3fn or uint8")
+        _check_dev(k, "k", on_device=False)
+        _check_dev(self.v, "v", k.dtype, tuple(k.shape), on_device=False)
+        _check_dev(self.k_scale, "k_scale", torch.float32, tuple(k.shape[:2]), on_device=False)
+        _check_dev(self.v_scale, "v_scale", torch.float32, tuple(k.shape[:2]), on_device=False)
+        pages, heads, page, dim = k.shape
+        _need(page in (16, 32, 64, 128), f"pages must hold 16, 32, 64 or 128 tokens, not {page}")
+        _need(dim % 16 == 0 and 16 <= dim <= 256, f"dim must be a multiple of 16 up to 256, not {dim}")
+        _on_device(k.device, ("v", self.v), ("k_scale", self.k_scale), ("v_scale", self.v_scale))
+        object.__setattr__(self, "_args", _CACHE_ARGS.pack(
+            k.data_ptr(), self.v.data_ptr(), self.k_scale.data_ptr(), self.v_scale.data_ptr(), pages, heads, page, dim))
+        object.__setattr__(self, "_shape", (pages, heads, page, dim))
+
+
+def kv_cache(pages: int, kv_heads: int, dim: int, page: int = 64, device="cuda") -> KVCache:
+    """A new, empty cache of `pages` pages of `page` tokens."""
+    kv = [torch.zeros((pages, kv_heads, page, dim), dtype=torch.uint8, device=device).view(torch.float8_e4m3fn)
+          for _ in range(2)]
+    scales = [torch.zeros((pages, kv_heads), dtype=torch.float32, device=device) for _ in range(2)]
+    return KVCache(kv[0], kv[1], scales[0], scales[1])
+
+
+def _pages_of(page_table: torch.Tensor):
+    _need(isinstance(page_table, torch.Tensor) and page_table.dtype == torch.int32 and page_table.dim() == 2
+          and (page_table.stride(1) == 1 or page_table.shape[1] < 2),
+          "page_table must be an int32 tensor (sequences, pages), each row contiguous")
+    S, n = page_table.shape
+    return page_table.data_ptr(), S, n, max(page_table.stride(0), n)
+
+
+def kv_append(k: torch.Tensor, v: torch.Tensor, cache: KVCache, page_table: torch.Tensor, kv_lens: torch.Tensor,
+              cu_new: torch.Tensor, table: Optional[torch.Tensor] = None, layout: str = "half",
+              q: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None) -> Optional[torch.Tensor]:
+    """Rotate the newest tokens' keys (and q), round keys and values to 8 bits
+    and put them into the cache (patch_kv_append).  k, v [tokens, kv_heads,
+    dim]; q [tokens, heads, dim] or None; page_table int32 [sequences,
+    pages]; kv_lens int32 [sequences], lengths with the new tokens; cu_new
+    int32 [sequences + 1], where each sequence's tokens begin; table of
+    rope_table, or None for no rotation.  Returns the rotated q (q_out,
+    which may be q), or None."""
+    lib = _lib or load()
+    _need(isinstance(cache, KVCache), "cache must be a KVCache")
+    _need(layout in _LAYOUTS, f"layout must be one of {sorted(_LAYOUTS)}, not {layout!r}")
+    _need(isinstance(k, torch.Tensor) and k.dim() == 3, "k must be a 3-D tensor (tokens, kv_heads, dim)")
+    _need(k.dtype in (torch.float16, torch.bfloat16), "k must be float16 or bfloat16")
+    _, hk, _, D = cache._shape
+    T = k.shape[0]
+    kp, kt, kh = _heads(k, "k", k.dtype, (T, hk, D))
+    vp, vt, vh = _heads(v, "v", k.dtype, (T, hk, D))
+    pp, S, max_pages, row = _pages_of(page_table)
+    lens, cu = _index(kv_lens, "kv_lens", S), _index(cu_new, "cu_new", S + 1)
+    tp, context, rot = _table_of(table)
+    _on_device(k.device, ("cache", cache.k), ("v", v), ("q", q), ("q_out", q_out), ("page_table", page_table),
+               ("kv_lens", kv_lens), ("cu_new", cu_new), ("table", table))
+    qp = qt = qh = op = ot = oh = heads = 0
+    if q is not None:
+        qp, qt, qh = _heads(q, "q", k.dtype, (T, None, D))
+        heads = q.shape[1]
+        if q_out is None:
+            q_out = torch.empty((T, heads, D), dtype=k.dtype, device=k.device)
+        op, ot, oh = _heads(q_out, "q_out", k.dtype, (T, heads, D))
+    else:
+        _need(q_out is None, "q_out without q")
+    _call(k.device, lib.patch_kv_append,
+          _APPEND_ARGS.pack(_TORCH_DT[k.dtype], _LAYOUTS[layout], T, S, heads, rot, context, max_pages, kp, kt, kh, vp, vt,
+                            vh, qp, qt, qh, op, ot, oh, pp, row, lens, cu, tp), cache._args)
+    return q_out
+
+
+def attention_workspace_bytes(tokens: int, sequences: int, heads: int, kv_heads: int, dim: int) -> int:
+    """Scratch that lets attention split long sequences (patch_attention_workspace_bytes)."""
+    return int((_lib or load()).patch_attention_workspace_bytes(tokens, sequences, heads, kv_heads, dim))
+
+
+def attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, kv_lens: torch.Tensor, cu_new: torch.Tensor,
+              scale: Optional[float] = None, window: int = 0, out_dtype: Optional[torch.dtype] = None,
+              out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None, workspace="auto") -> torch.Tensor:
+    """softmax(scale q k^T) v over the cache for every sequence's newest
+    tokens, which were appended before (patch_attention): q [tokens, heads,
+    dim], heads a multiple of the cache's; page_table, kv_lens and cu_new as
+    for kv_append.  A token sees the keys up to its own position, with window
+    > 0 the last `window` of them.  scale: 1 / sqrt(dim) if not given.  lse:
+    float32 [tokens, heads] to take the logarithm of each softmax's sum.
+    workspace as for gemm."""
+    lib = _lib or load()
+    _need(isinstance(cache, KVCache), "cache must be a KVCache")
+    _need(isinstance(q, torch.Tensor) and q.dim() == 3, "q must be a 3-D tensor (tokens, heads, dim)")
+    _need(q.dtype in (torch.float16, torch.bfloat16), "q must be float16 or bfloat16")
+    _, hk, _, D = cache._shape
+    T, H, _ = q.shape
+    qp, qt, qh = _heads(q, "q", q.dtype, (T, H, D))
+    pp, S, max_pages, row = _pages_of(page_table)
+    lens, cu = _index(kv_lens, "kv_lens", S), _index(cu_new, "cu_new", S + 1)
+    od = out_dtype or q.dtype
+    _check_out_dtype(od, q.dtype)
+    _on_device(q.device, ("cache", cache.k), ("page_table", page_table), ("kv_lens", kv_lens), ("cu_new", cu_new),
+               ("out", out), ("lse", lse))
+    if out is None:
+        out = torch.empty((T, H, D), dtype=od, device=q.device)
+    op, ot, oh = _heads(out, "out", od, (T, H, D))
+    if lse is not None:
+        _check_dev(lse, "lse", torch.float32, (T, H))
+    ws, nb = None, 0
+    if workspace is not None:
+        nb = _ws_bytes("attention", (T, S), (H, hk), D, q.device.index,
+                       lambda: lib.patch_attention_workspace_bytes(T, S, H, hk, D))
+        ws = _workspace(nb, workspace, q.device)
+        nb = 0 if ws is None else ws.numel() * ws.element_size()
+    _call(q.device, lib.patch_attention,
+          _ATTENTION_ARGS.pack(_TORCH_DT[q.dtype], _TORCH_DT[od], T, S, H, max_pages, window,
+                               D ** -0.5 if scale is None else scale, qp, qt, qh, op, ot, oh,
+                               0 if lse is None else lse.data_ptr(), pp, row, lens, cu),
+          cache._args, None if ws is None else ws.data_ptr(), nb)
+    return out
+
+
+@dataclasses.dataclass(frozen=True)
+class W4Weight:
+    """A weight of 4-bit values and group scales, laid out for w4_gemm."""
+    packed: torch.Tensor  # uint8, device
+    dtype: torch.dtype    # of the scales and of X
+    N: int
+    K: int
+    group: int
+    with_zero: bool
+
+
+def w4_quantize(W: torch.Tensor, group: int = 128, zero: bool = False):
+    """W (N x K, float16 or bfloat16) rounded to 4 bits a group of `group`
+    columns (patch_w4_quantize): returns q uint8 [N, K / 2], scale [N, K /
+    group] of W's type, and with zero=True the zeros uint8 [N, K / group],
+    else None."""
+    lib = _lib or load()
+    _need(isinstance(W, torch.Tensor) and W.dim() == 2, "W must be a 2-D tensor (N x K)")
+    _need(W.dtype in (torch.float16, torch.bfloat16), "W must be float16 or bfloat16")
+    _check_dev(W, "W", on_device=False)
+    N, K = W.shape
+    _need(group in (32, 64, 128) and K % group == 0 and N > 0 and K > 0, f"K={K} must be a multiple of the group ({group}: 32, 64 or 128)")
+    _on_device(W.device)
+    q = torch.empty((N, K // 2), dtype=torch.uint8, device=W.device)
+    scale = torch.empty((N, K // group), dtype=W.dtype, device=W.device)
+    z = torch.empty((N, K // group), dtype=torch.uint8, device=W.device) if zero else None
+    _call(W.device, lib.patch_w4_quantize, _TORCH_DT[W.dtype], N, K, group, W.data_ptr(), q.data_ptr(), scale.data_ptr(),
+          None if z is None else z.data_ptr())
+    return q, scale, z
+
+
+def w4_pack(q: torch.Tensor, scale: torch.Tensor, zero: Optional[torch.Tensor], group: int) -> W4Weight:
+    """Lay 4-bit weights out for w4_gemm (patch_w4_pack): q uint8 [N, K / 2],
+    the even column in a byte's low half; scale [N, K / group]; zero uint8
+    [N, K / group], or None for 8 everywhere."""
+    lib = _lib or load()
+    _need(isinstance(q, torch.Tensor) and q.dim() == 2, "q must be a 2-D tensor (N x K / 2)")
+    _check_dev(q, "q", torch.uint8, on_device=False)
+    N, K = q.shape[0], 2 * q.shape[1]
+    _need(group in (32, 64, 128) and K % group == 0 and N > 0 and K > 0, f"K={K} must be a multiple of the group ({group}: 32, 64 or 128)")
+    _check_dev(scale, "scale", shape=(N, K // group), on_device=False)
+    _need(scale.dtype in (torch.float16, torch.bfloat16), "scale must be float16 or bfloat16")
+    if zero is not None:
+        _check_dev(zero, "zero", torch.uint8, (N, K // group), on_device=False)
+    _on_device(q.device, ("scale", scale), ("zero", zero))
+    packed = torch.empty(int(lib.patch_w4_bytes(N, K, group, zero is not None)), dtype=torch.uint8, device=q.device)
+    _call(q.device, lib.patch_w4_pack, _TORCH_DT[scale.dtype], N, K, group, q.data_ptr(), scale.data_ptr(),
+          None if zero is None else zero.data_ptr(), packed.data_ptr(), packed.numel())
+    return W4Weight(packed, scale.dtype, N, K, group, zero is not None)
+
+
+def w4_gemm(X: torch.Tensor, weight: W4Weight, out_dtype: Optional[torch.dtype] = None,
+            out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Y = X W^T with 4-bit weights (patch_w4_gemm)."""
+    lib = _lib or load()
+    _need(isinstance(weight, W4Weight), "weight must be a W4Weight (w4_pack)")
+    _check_x(X, weight.dtype, weight.K)
+    M = X.shape[0]
+    od = out_dtype or X.dtype
+    _check_out_dtype(od, X.dtype)
+    _check_out(out, (M, weight.N), od)
+    _on_device(X.device, ("weight", weight.packed), ("out", out))
+    if out is None:
+        out = torch.empty((M, weight.N), dtype=od, device=X.device)
+    _call(X.device, lib.patch_w4_gemm, _TORCH_DT[weight.dtype], weight.N, weight.K, weight.group, weight.with_zero,
+          weight.packed.data_ptr(), weight.packed.numel(), X.data_ptr(), M, out.data_ptr(), _TORCH_DT[od])
+    return out
