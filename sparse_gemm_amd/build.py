@@ -15,7 +15,7 @@ CSRC = os.path.join(HERE, "csrc")
 OBJ = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libpatch.so")
 SOURCES = ["pack.hip", "gemm_decode.hip", "gemm_prefill.hip", "gemm_prefill_big.hip", "sampler.hip", "fine_mask.hip", "probe.hip", "noalloc.hip",
-           "rope.hip", "kv_append.hip", "attention.hip", "gemm_w4.hip", "patch_api.cpp", "layer_api.cpp"]
+           "rope.hip", "kv_append.hip", "attention.hip", "attention_chunk.hip", "gemm_w4.hip", "patch_api.cpp", "layer_api.cpp"]
 ARCH = "gfx950"
 
 

@@ -49,131 +49,13 @@
 #include <atomic>
 #include <random>
 
-#include "device_common.h"
-#include "layer_common.h"
+#include "attention_common.h"
 
 namespace patch {
+using namespace attn;
 namespace {
 
-#ifndef KW
-#define KW 4
-#endif
-#ifndef KM
-#define KM 8
-#endif
-constexpr int kWaves = KW;
-constexpr int kThreads = 64 * kWaves;
-constexpr int kStep = 32;       // keys of a step
-#ifndef KC
-#define KC 8
-#endif
-constexpr int kTaskCost = KC;   // of a task beside its steps, in steps
-constexpr int kMinSteps = KM;    // steps of a workgroup, at least
-constexpr float kBias = 14.0f;  // probabilities are 2^(s - m + kBias)
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kInf = __builtin_inff();
-
-struct Args {
-  const uint16_t* q;
-  void* out;
-  float* lse;
-  const int32_t *table, *lens, *cu;
-  const uint8_t *k, *v;
-  const float *ks, *vs;
-  float* parts;     // [worker][2][rows][DP + 2]
-  uint64_t* flags;  // [worker][2]
-  uint64_t token;
-  int64_t q_token, q_head, o_token, o_head, table_row;
-  int T, S, heads, kv_heads, group, D, B, shift, pages, max_pages, window;
-  float scale;  // with log2(e)
-  bool q_wide, o_wide, out_f32;
-};
-
-__device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
-__device__ __forceinline__ float finite_or_0(float m) { return m == -kInf ? 0.f : m; }
-
-// Two (lo or hi half of a word) e4m3 bytes as two 16-bit values.
-template <bool BF16, bool HI>
-__device__ __forceinline__ uint32_t widen2(uint32_t w) {
-  if constexpr (BF16)
-    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, HI));
-  else
-    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, HI));
-}
-template <bool BF16>
-__device__ __forceinline__ u32x4 widen8(uint32_t lo, uint32_t hi) {
-  return (u32x4){widen2<BF16, false>(lo), widen2<BF16, true>(lo), widen2<BF16, false>(hi), widen2<BF16, true>(hi)};
-}
-
-// Four neighbouring elements of 8 keys (a word a key) as four A operands of
-// V^T, a byte of each key.
-__device__ __forceinline__ void zip4(const uint32_t (&v)[8], u32x4 (&e)[4]) {
-#pragma unroll
-  for (int p = 0; p < 4; p++) {
-    const uint32_t z0 = __builtin_amdgcn_perm(v[2 * p + 1], v[2 * p], 0x05010400u);
-    const uint32_t z1 = __builtin_amdgcn_perm(v[2 * p + 1], v[2 * p], 0x07030602u);
-    e[0][p] = widen2<false, false>(z0);
-    e[1][p] = widen2<false, true>(z0);
-    e[2][p] = widen2<false, false>(z1);
-    e[3][p] = widen2<false, true>(z1);
-  }
-}
-
-// A sequence's newest tokens c0 .. c0 + n - 1, the position of the first, and
-// whether its length does not fit its page table.
-struct Seq {
-  int c0, n, past;
-  bool bad;
-};
-__device__ __forceinline__ Seq seq_of(const Args& a, int s) {
-  Seq q;
-  const int e = min(a.cu[s + 1], a.T), len = a.lens[s];
-  q.c0 = max(a.cu[s], 0);
-  q.n = max(e - q.c0, 0);
-  q.past = max(len, -0x40000000) - q.n;
-  q.bad = len > a.max_pages << a.shift;
-  return q;
-}
-
-// The rows r0 .. r1 - 1 of a task and the steps of the keys they see.
-struct Task {
-  int r0, r1, first_pos, last_pos, begin, end;
-  bool fill;  // nothing to attend to: rows are filled
-};
-template <int ROWS>
-__device__ __forceinline__ Task task_of(const Args& a, const Seq& sq, int rt) {
-  Task t;
-  t.r0 = rt * ROWS;
-  t.r1 = min(t.r0 + ROWS, sq.n * a.group);
-  t.first_pos = sq.past + t.r0 / a.group;
-  t.last_pos = sq.past + (t.r1 - 1) / a.group;
-  t.fill = sq.bad || t.last_pos < 0;
-  const int from = a.window > 0 ? max(t.first_pos - a.window + 1, 0) : 0;
-  t.begin = t.fill ? 0 : from / kStep;
-  t.end = t.fill ? 1 : t.last_pos / kStep + 1;
-  return t;
-}
-// A head's cost on the line: its tasks' steps, and kTaskCost for each task.
-template <int ROWS>
-__device__ __forceinline__ int cost_of(const Args& a, const Seq& sq) {
-  const int tiles = (sq.n * a.group + ROWS - 1) / ROWS;
-  int n = 0;
-  for (int i = 0; i < tiles; i++) {
-    const Task t = task_of<ROWS>(a, sq, i);
-    n += t.end - t.begin + kTaskCost;
-  }
-  return n;
-}
-// The pieces a head's tasks make at kMinSteps or more steps each.
-__device__ __forceinline__ int pieces_of(const Task& t) { return (t.end - t.begin + kMinSteps - 1) / kMinSteps; }
-template <int ROWS>
-__device__ __forceinline__ int pieces_of(const Args& a, const Seq& sq) {
-  const int tiles = (sq.n * a.group + ROWS - 1) / ROWS;
-  int n = 0;
-  for (int i = 0; i < tiles; i++) n += pieces_of(task_of<ROWS>(a, sq, i));
-  return n;
-}
+constexpr int kStep = 32;  // keys of a step
 
 // The pages of a wave's next 64 steps, one step a lane; h: halves of a step
 // (16 keys lie in one page).  A page outside the cache reads page 0 with a
@@ -198,11 +80,6 @@ __device__ __forceinline__ Pages load_pages(const Args& a, const int32_t* table,
   }
   return p;
 }
-__device__ __forceinline__ int lane_of(int v, int i) { return __builtin_amdgcn_readlane(v, i); }
-__device__ __forceinline__ float lane_of(float v, int i) {
-  return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), i));
-}
-
 // The bytes of a step: K as A operands, V in bytes [key slot][element].
 template <int DP>
 struct Bytes {
@@ -422,63 +299,16 @@ __device__ __forceinline__ void do_step(const Args& a, const Task& task, int ste
   }
 }
 
-// Eight neighbouring outputs.
-template <bool BF16>
-__device__ __forceinline__ void store8(const Args& a, int64_t at, const float (&v)[8]) {
-  if (a.out_f32) {
-    float* op = reinterpret_cast<float*>(a.out) + at;
-    if (a.o_wide) {
-      *reinterpret_cast<f32x4*>(op) = (f32x4){v[0], v[1], v[2], v[3]};
-      *reinterpret_cast<f32x4*>(op + 4) = (f32x4){v[4], v[5], v[6], v[7]};
-    } else {
-      for (int i = 0; i < 8; i++) op[i] = v[i];
-    }
-  } else {
-    typedef std::conditional_t<BF16, __bf16, _Float16> T;
-    Vec<T, 8> o;
-#pragma unroll
-    for (int i = 0; i < 8; i++) o.v[i] = (T)v[i];
-    T* op = reinterpret_cast<T*>(a.out) + at;
-    if (a.o_wide) {
-      *reinterpret_cast<Vec<T, 8>*>(op) = o;
-    } else {
-      for (int i = 0; i < 8; i++) op[i] = o.v[i];
-    }
-  }
-}
-__device__ __forceinline__ int64_t out_at(const Args& a, const Seq& sq, int h, int row, int d) {
-  const int tok = row / a.group, head = h * a.group + row - tok * a.group;
-  return (int64_t)(sq.c0 + tok) * a.o_token + (int64_t)head * a.o_head + d;
-}
-__device__ __forceinline__ void store_lse(const Args& a, const Seq& sq, int h, int row, float v) {
-  const int tok = row / a.group, head = h * a.group + row - tok * a.group;
-  a.lse[(int64_t)(sq.c0 + tok) * a.heads + head] = v;
-}
-__device__ __forceinline__ float lse_of(float m, float l) { return (m + __log2f(l) - kBias) * kLn2; }
-
-template <bool BF16>
-__device__ __forceinline__ void fill_rows(const Args& a, const Seq& sq, const Task& t, int h) {
-  const float o = sq.bad ? __builtin_nanf("") : 0.f, lse = sq.bad ? __builtin_nanf("") : -kInf;
-  const int chunks = a.D / 8;
-  for (int e = threadIdx.x; e < (t.r1 - t.r0) * chunks; e += kThreads) {
-    const int row = t.r0 + e / chunks, d = e % chunks * 8;
-    store8<BF16>(a, out_at(a, sq, h, row, d), {o, o, o, o, o, o, o, o});
-    if (a.lse && d == 0) store_lse(a, sq, h, row, lse);
-  }
-}
-
-constexpr int kCoherent = 16;  // cache policy bits of a buffer access: sc1
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* p, uint32_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)bytes, 0x00020000);
-}
-
-// The steps begin .. end - 1 of a task, by the whole workgroup.  part < 0:
-// they are all of its steps, and the rows are stored.  Else o / l, m and l go
-// to slot `part` of the workspace.
 template <bool BF16, int DP, int R>
-__device__ __forceinline__ void run_steps(const Args& a, const Seq& sq, const Task& task, int s, int h, int begin,
+struct Few {
+  static constexpr bool kBf16 = BF16;
+  static constexpr int kDim = DP, kRows = 16 * R, kStep = patch::kStep, kMinSteps = 8, kTaskCost = 8;
+  static constexpr int kPerCu = R == 1 && DP <= 128 ? 2 : 1;
+  static constexpr int kLds = kWaves * kRows * (DP + 4) + kWaves * kRows * 2 + kWaves;
+
+  static __device__ __forceinline__ void run(const Args& a, const Seq& sq, const Task& task, int s, int h, int begin,
                                           int end, int part, float* lds) {
-  constexpr int kRows = 16 * R, kLd = DP + 4, VB = DP / 16;
+  constexpr int kLd = DP + 4, VB = DP / 16;
   const int tid = (int)threadIdx.x, lane = tid & 63, wave = tid >> 6, n = lane & 15, g = lane >> 4;
   Rows<BF16, DP, R> x;
   const int32_t* table = a.table + s * a.table_row;
@@ -560,242 +390,26 @@ __device__ __forceinline__ void run_steps(const Args& a, const Seq& sq, const Ta
     }
   }
 }
-
-// Join the parts of a task: slot 1 of worker w0, then slot 0 of the next.
-template <bool BF16, int DP, int R>
-__device__ __forceinline__ void join_parts(const Args& a, const Seq& sq, const Task& task, int h, int w0, int count) {
-  constexpr int kRows = 16 * R, kSlot = kRows * (DP + 2);
-  const int chunks = a.D / 8;
-  for (int e = threadIdx.x; e < (task.r1 - task.r0) * chunks; e += kThreads) {
-    const int row = e / chunks, d = (e - row * chunks) * 8;
-    float mx = -kInf, sum = 0.f, acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-    for (int p = 0; p < count; p++) {
-      const int64_t slot = 2 * ((int64_t)w0 + p) + (p == 0);
-      const __amdgpu_buffer_rsrc_t rs = rsrc(a.parts + slot * kSlot, kSlot * 4);
-      const int at = (row * DP + d) * 4;
-      const u32x2 ml = __builtin_amdgcn_raw_buffer_load_b64(rs, (kRows * DP + 2 * row) * 4, 0, kCoherent);
-      const f32x4 lo = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, at, 0, kCoherent));
-      const f32x4 hi = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, at + 16, 0, kCoherent));
-      const float m = __uint_as_float(ml[0]), l = __uint_as_float(ml[1]);
-      const float mn = fmaxf(mx, m), mu = finite_or_0(mn);
-      const float f = exp2_(mx - mu), w = exp2_(m - mu) * l;
-      mx = mn;
-      sum = sum * f + w;
-#pragma unroll
-      for (int i = 0; i < 4; i++) {
-        acc[i] = acc[i] * f + w * lo[i];
-        acc[4 + i] = acc[4 + i] * f + w * hi[i];
-      }
-    }
-    const float inv = sum == 0.f ? 0.f : 1.0f / sum;
-#pragma unroll
-    for (int i = 0; i < 8; i++) acc[i] *= inv;
-    store8<BF16>(a, out_at(a, sq, h, task.r0 + row, d), acc);
-    if (a.lse && d == 0) store_lse(a, sq, h, task.r0 + row, lse_of(mx, sum));
-  }
-}
-
-template <int DP, int R>
-constexpr int lds_floats() {
-  return kWaves * 16 * R * (DP + 4) + kWaves * 16 * R * 2 + kWaves;
-}
-
-// A sequence, where it begins and ends on a line.
-struct Place {
-  int s, from, to;
 };
 
-// A line over up to 64 sequences, one a lane; every wave has its own.
-struct LaneLine {
-  int from, to, total;
-  __device__ __forceinline__ explicit LaneLine(int n) {
-    const int lane = (int)threadIdx.x & 63;
-    to = n;
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-      const int v = __shfl_up(to, d);
-      if (lane >= d) to += v;
-    }
-    from = to - n;
-    total = lane_of(to, 63);
-  }
-  __device__ __forceinline__ Place find(int u) const {
-    const int s = __builtin_ctzll(__ballot(to > u));  // the first that ends behind u
-    return Place{s, lane_of(from, s), lane_of(to, s)};
-  }
-};
+// Many rows a sequence on average: attention_chunk.hip.
+bool many_rows(int64_t T, int64_t S, int64_t group, int64_t dim) { return dim <= 128 && T * group > 32 * S; }
 
-// For more sequences: a prefix sum in LDS, by the whole workgroup.
-struct LdsLine {
-  int* line;  // [S + 1]: where sequence s begins
-  int total, S;
-  template <typename F>
-  __device__ __forceinline__ LdsLine(int n_seqs, int* l, int* wave_sum, F cost) : line(l), total(0), S(n_seqs) {
-    const int tid = (int)threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int each = (S + kThreads - 1) / kThreads, s1 = min((tid + 1) * each, S);
-    int mine = 0;
-    for (int s = tid * each; s < s1; s++) {
-      line[s] = cost(s);
-      mine += line[s];
-    }
-    int upto = mine;
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-      const int v = __shfl_up(upto, d);
-      if (lane >= d) upto += v;
-    }
-    if (lane == 63) wave_sum[wave] = upto;
-    __syncthreads();
-    int at = upto - mine;
-    for (int w = 0; w < kWaves; w++) {
-      if (w < wave) at += wave_sum[w];
-      total += wave_sum[w];
-    }
-    for (int s = tid * each; s < s1; s++) {
-      const int n = line[s];
-      line[s] = at;
-      at += n;
-    }
-    if (tid == 0) line[S] = total;
-    __syncthreads();
-  }
-  __device__ __forceinline__ Place find(int u) const {
-    // the last that begins at or before u: of equal ones the one with steps
-    const int s = find_last(S, [&](int i) { return line[i] <= u; });
-    return Place{s, line[s], line[s + 1]};
-  }
-};
+// Sixteens of rows of a task, by the rows a sequence has on average.
+int tile_rows(int64_t T, int64_t S, int64_t group, int64_t dim) { return T * group <= 16 * S || dim > 128 ? 1 : 2; }
 
-// Steps begin .. end - 1 of a task by this workgroup, one of the task's
-// `count` parts, which the workgroups w0 .. w0 + count - 1 have: part 0 in
-// slot 1 of its workgroup, the others in slot 0.
-template <bool BF16, int DP, int R>
-__device__ __forceinline__ void run_piece(const Args& a, const Seq& sq, const Task& task, int s, int h, int begin,
-                                          int end, int w0, int count, float* lds, int* joined) {
-  if (task.fill) {
-    fill_rows<BF16>(a, sq, task, h);
-    return;
-  }
-  const int lane = (int)threadIdx.x & 63;
-  const int mine = count == 1 ? -1 : 2 * (int)blockIdx.x + ((int)blockIdx.x == w0 ? 1 : 0);
-  run_steps<BF16, DP, R>(a, sq, task, s, h, begin, end, mine, lds);
-  if (count > 1) {
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's share of the part has arrived
-    __syncthreads();
-    if (threadIdx.x < 64) {
-      if (lane == 0) {
-        const uint64_t old =
-            __hip_atomic_exchange(a.flags + mine, a.token, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        asm volatile("" ::"v"(old));
-      }
-      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // and its flag, before the others' are read
-      bool all = true;
-      for (int p = lane; p < count; p += 64)
-        all &= __hip_atomic_load(a.flags + 2 * (w0 + p) + (p == 0), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
-               a.token;
-      const bool done = __ballot(!all) == 0;
-      if (lane == 0) *joined = done;
-      if (done)
-        for (int p = lane; p < count; p += 64)
-          __hip_atomic_store(a.flags + 2 * (w0 + p) + (p == 0), (uint64_t)0, __ATOMIC_RELAXED,
-                             __HIP_MEMORY_SCOPE_AGENT);
-    }
-    __syncthreads();
-    if (*joined) join_parts<BF16, DP, R>(a, sq, task, h, w0, count);
-  }
+template <bool BF16>
+hipError_t by_shape(Args& a, void* ws, uint64_t ws_bytes, hipStream_t s) {
+  if (many_rows(a.T, a.S, a.group, a.D)) return launch_attention_chunk(BF16, a, ws, ws_bytes, s);
+  const int R = tile_rows(a.T, a.S, a.group, a.D);
+  if (a.D <= 64) return R == 1 ? go<Few<BF16, 64, 1>>(a, ws, ws_bytes, s) : go<Few<BF16, 64, 2>>(a, ws, ws_bytes, s);
+  if (a.D <= 128) return R == 1 ? go<Few<BF16, 128, 1>>(a, ws, ws_bytes, s) : go<Few<BF16, 128, 2>>(a, ws, ws_bytes, s);
+  return go<Few<BF16, 256, 1>>(a, ws, ws_bytes, s);
 }
 
-// All work on one line (see the top).  Where there are fewer pieces of
-// kMinSteps steps than workgroups, each task is cut evenly and every piece
-// has a workgroup.  Else workgroup w takes the w-th equal piece of the line,
-// on which a task begins with kTaskCost places that stand for what it costs
-// beside its steps: about what that many steps take.
-template <bool BF16, int DP, int R, bool MANY>
-__global__ __launch_bounds__(kThreads, (R == 1 && DP <= 128 ? 8 : 4) / kWaves) void k_attention_line(Args a) {
-  extern __shared__ __align__(16) float lds[];
-  __shared__ int wave_sum[kWaves];
-  __shared__ int joined;
-  constexpr int kRows = 16 * R;
-  Seq mine{0, 0, 0, false};  // of this lane's sequence
-  if constexpr (!MANY) {
-    const int lane = (int)threadIdx.x & 63;
-    if (lane < a.S) mine = seq_of(a, lane);
-    const LaneLine pieces(lane < a.S ? pieces_of<kRows>(a, mine) * a.kv_heads : 0);
-    if (pieces.total <= (int)gridDim.x) {
-      if ((int)blockIdx.x >= pieces.total) return;
-      const Place pl = pieces.find((int)blockIdx.x);
-      const Seq sq{lane_of(mine.c0, pl.s), lane_of(mine.n, pl.s), lane_of(mine.past, pl.s), lane_of((int)mine.bad, pl.s) != 0};
-      const int per_head = (pl.to - pl.from) / a.kv_heads, h = ((int)blockIdx.x - pl.from) / per_head;
-      int w0 = pl.from + h * per_head, rt = 0;
-      Task task = task_of<kRows>(a, sq, 0);
-      int count = pieces_of(task);
-      while (w0 + count <= (int)blockIdx.x) {
-        w0 += count;
-        task = task_of<kRows>(a, sq, ++rt);
-        count = pieces_of(task);
-      }
-      const int i = (int)blockIdx.x - w0, steps = task.end - task.begin;
-      const int each = steps / count, more = steps - each * count;  // the first `more` pieces have one step more
-      const int begin = task.begin + i * each + min(i, more);
-      run_piece<BF16, DP, R>(a, sq, task, pl.s, h, begin, begin + each + (i < more ? 1 : 0), w0, count, lds, &joined);
-      return;
-    }
-  }
-  const auto line = [&] {
-    if constexpr (MANY)
-      return LdsLine(a.S, reinterpret_cast<int*>(lds + lds_floats<DP, R>()), wave_sum,
-                     [&](int s) { return cost_of<kRows>(a, seq_of(a, s)) * a.kv_heads; });
-    else
-      return LaneLine(((int)threadIdx.x & 63) < a.S ? cost_of<kRows>(a, mine) * a.kv_heads : 0);
-  }();
-  const int per = (line.total + (int)gridDim.x - 1) / (int)gridDim.x;
-  int u = per * (int)blockIdx.x;
-  const int u_end = min(u + per, line.total);
-  while (u < u_end) {
-    const Place pl = line.find(u);
-    const Seq sq = MANY ? seq_of(a, pl.s)
-                        : Seq{lane_of(mine.c0, pl.s), lane_of(mine.n, pl.s), lane_of(mine.past, pl.s),
-                              lane_of((int)mine.bad, pl.s) != 0};
-    const int per_head = (pl.to - pl.from) / a.kv_heads, h = (u - pl.from) / per_head;
-    int at = pl.from + h * per_head, rt = 0;  // where the task begins on the line
-    Task task = task_of<kRows>(a, sq, 0);
-    while (at + (task.end - task.begin) + kTaskCost <= u) {
-      at += task.end - task.begin + kTaskCost;
-      task = task_of<kRows>(a, sq, ++rt);
-    }
-    at += kTaskCost;  // its first step
-    const int task_end = at + (task.end - task.begin), from = max(u, at), to = min(u_end, task_end);
-    if (from < to) {
-      const int w0 = at / per;
-      run_piece<BF16, DP, R>(a, sq, task, pl.s, h, task.begin + from - at, task.begin + to - at, w0,
-                             (task_end - 1) / per - w0 + 1, lds, &joined);
-      __syncthreads();  // LDS is used again
-    }
-    u = task_end;
-  }
-}
+}  // namespace
 
-// Without a workspace: a workgroup a task.  Sequence s has the tasks
-// floor(cu[s] group / rows) + s up to the same of s + 1 for each head, at
-// least as many as its rows need.
-template <bool BF16, int DP, int R>
-__global__ __launch_bounds__(kThreads) void k_attention_task(Args a) {
-  extern __shared__ __align__(16) float lds[];
-  constexpr int kRows = 16 * R;
-  const int h = (int)(blockIdx.x % (uint32_t)a.kv_heads);
-  const int64_t slot = blockIdx.x / (uint32_t)a.kv_heads;
-  const int s = find_last(a.S, [&](int i) { return (int64_t)a.cu[i] * a.group / kRows + i <= slot; });
-  const int64_t first = (int64_t)a.cu[s] * a.group / kRows + s;
-  const Seq sq = seq_of(a, s);
-  if (slot < first || (slot - first) * kRows >= (int64_t)sq.n * a.group) return;
-  const Task task = task_of<kRows>(a, sq, (int)(slot - first));
-  if (task.fill)
-    fill_rows<BF16>(a, sq, task, h);
-  else
-    run_steps<BF16, DP, R>(a, sq, task, s, h, task.begin, task.end, -1, lds);
-}
-
+namespace attn {
 // A value of this launch for the flags: a counter mixed with a random salt of
 // the process (splitmix64's finaliser), never 0.
 uint64_t launch_token() {
@@ -811,59 +425,14 @@ uint64_t launch_token() {
   return z == 0 ? 1 : z;
 }
 
-// Rows of a task in sixteens: by the rows a sequence has on average.
-int tile_rows(int64_t T, int64_t S, int64_t group, int64_t dim) {
-  const int64_t rows = T * group;
-  return rows <= 16 * S || dim > 128 ? 1 : 2;
-}
-int workers_of(int R, int DP) { return cu_count() * (R == 1 && DP <= 128 ? 8 : 4) / kWaves; }
-constexpr int padded_dim(int64_t dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
-uint64_t slot_bytes(int R, int DP) { return (uint64_t)(16 * R * (DP + 2)) * 4; }
-
-hipError_t launch(const void* fn, int64_t blocks, size_t lds, Args& a, hipStream_t s) {
-  if (blocks > 0x7fffffff) return hipErrorInvalidValue;
-  if (lds > 65536) {
-    hipError_t e = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-    if (e != hipSuccess) return e;
-  }
-  void* args[] = {&a};
-  return hipLaunchKernel(fn, dim3((unsigned)blocks), dim3(kThreads), args, lds, s);
-}
-
-template <bool BF16, int DP, int R>
-hipError_t go(Args& a, void* ws, uint64_t ws_bytes, hipStream_t s) {
-  const uint64_t workers = (uint64_t)workers_of(R, DP);
-  const size_t lds = sizeof(float) * (size_t)lds_floats<DP, R>();
-  // the line's places are 32-bit numbers
-  const int64_t tasks = ((int64_t)a.T * a.group / (16 * R) + a.S) * a.kv_heads;
-  const int64_t steps = (((int64_t)a.max_pages << a.shift) + kStep - 1) / kStep + 1 + kTaskCost;
-  const bool fits = tasks < 0x40000000 && tasks * steps < 0x40000000;
-  if (fits && ws && ws_bytes >= workers * 2 * (slot_bytes(R, DP) + 8)) {
-    a.flags = reinterpret_cast<uint64_t*>(ws);
-    a.parts = reinterpret_cast<float*>(a.flags + 2 * workers);
-    a.token = launch_token();
-    return a.S > 64 ? launch(reinterpret_cast<const void*>(k_attention_line<BF16, DP, R, true>), (int64_t)workers,
-                             lds + 4 * (size_t)(a.S + 1), a, s)
-                    : launch(reinterpret_cast<const void*>(k_attention_line<BF16, DP, R, false>), (int64_t)workers, lds,
-                             a, s);
-  }
-  return launch(reinterpret_cast<const void*>(k_attention_task<BF16, DP, R>),
-                tasks, lds, a, s);
-}
-
-template <bool BF16>
-hipError_t by_shape(Args& a, void* ws, uint64_t ws_bytes, hipStream_t s) {
-  const int R = tile_rows(a.T, a.S, a.group, a.D);
-  if (a.D <= 64) return R == 1 ? go<BF16, 64, 1>(a, ws, ws_bytes, s) : go<BF16, 64, 2>(a, ws, ws_bytes, s);
-  if (a.D <= 128) return R == 1 ? go<BF16, 128, 1>(a, ws, ws_bytes, s) : go<BF16, 128, 2>(a, ws, ws_bytes, s);
-  return go<BF16, 256, 1>(a, ws, ws_bytes, s);
-}
-
-}  // namespace
+}  // namespace attn
 
 uint64_t attention_workspace_bytes(int64_t T, int64_t S, int64_t heads, int64_t kv_heads, int64_t dim) {
-  const int R = tile_rows(T, S, heads / kv_heads, dim), DP = padded_dim(dim);
-  return (uint64_t)workers_of(R, DP) * 2 * (slot_bytes(R, DP) + 8);
+  if (many_rows(T, S, heads / kv_heads, dim)) return attention_chunk_workspace_bytes(dim);
+  const int R = tile_rows(T, S, heads / kv_heads, dim);
+  if (dim <= 64) return R == 1 ? workspace_bytes<Few<true, 64, 1>>() : workspace_bytes<Few<true, 64, 2>>();
+  if (dim <= 128) return R == 1 ? workspace_bytes<Few<true, 128, 1>>() : workspace_bytes<Few<true, 128, 2>>();
+  return workspace_bytes<Few<true, 256, 1>>();
 }
 
 hipError_t launch_attention(const patch_attention_args& p, const patch_kv_cache& c, void* ws, uint64_t ws_bytes,

@@ -1,0 +1,354 @@
+// attention_chunk.hip -- attention over the paged 8-bit cache for many new
+// tokens a sequence (prompts and their chunks).
+//
+// Here the matrix cores and the exponentials bound the work, not the cache:
+// every row tile reads the same keys, mostly from L2.  So the four waves of a
+// workgroup have 16 R rows each and share the keys: a tile of 128 keys is
+// loaded once, each wave widening 32 of them into LDS as ready matrix
+// operands (lane order, 16 bytes a lane: reads and writes without bank
+// conflicts), and every wave then runs all 128 against its rows.  The next
+// tile's bytes are in registers by then.  Rows are a wave's own, so nothing is
+// joined at the end; two workgroups a CU fill each other's waits.
+//
+// The products, the running maximum and sum, and the order of the keys inside
+// an operand are those of attention.hip; 64 keys are treated at once.
+#include "attention_common.h"
+
+namespace patch {
+using namespace attn;
+namespace {
+
+constexpr int kTile = 128;           // keys of a tile (a step of the line)
+constexpr int kSubs = kTile / 16;    // its sub-tiles of 16 keys, each in one page
+
+// Waits for this wave's LDS traffic, not for loads from memory, and meets the others.
+__device__ __forceinline__ void meet() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+template <bool BF16, int DP, int R>
+struct Chunk {
+  static constexpr bool kBf16 = BF16;
+  static constexpr int kDim = DP, kRows = kWaves * 16 * R, kStep = kTile, kMinSteps = 4, kTaskCost = 2;
+  static constexpr int kPerCu = 2;
+  static constexpr int kFrags = DP / 16;                        // operands (1 KB) of 32 keys, of K as of V
+  static constexpr int kLds = kWaves * 2 * kFrags * 256 + 4;    // and a word that says that V held a NaN
+  static constexpr int VB = DP / 16;                            // bytes of a V row in a lane
+
+  // Pages of eight tiles, a sub-tile a lane.
+  struct Pages {
+    int page;
+    float ks, vs, vmax;  // vmax: the largest |v scale| of the lane's tile
+  };
+  static __device__ __forceinline__ Pages load_pages(const Args& a, const int32_t* table, int h, int tile, int last_pos) {
+    Pages p;
+    const int64_t key = min((int64_t)tile * kTile + 16 * (int64_t)(threadIdx.x & 63), (int64_t)(last_pos & ~15));
+    const int page = table[key >> a.shift];
+    const bool ok = page >= 0 && page < a.pages;
+    p.page = ok ? page : 0;
+    const int64_t at = (int64_t)p.page * a.kv_heads + h;
+    p.ks = ok ? a.ks[at] * a.scale : __builtin_nanf("");
+    p.vs = ok ? a.vs[at] : 0.f;
+    p.vmax = fabsf(p.vs);
+#pragma unroll
+    for (int d = 1; d < kSubs; d *= 2) p.vmax = fmaxf(p.vmax, __shfl_xor(p.vmax, d));
+    return p;
+  }
+  // Where sub-tile i's (of the tile's 8) first row lies.
+  static __device__ __forceinline__ int64_t row_at(const Args& a, const Pages& p, int base, int i, int h, int tile,
+                                                   int last_pos) {
+    const int key = min(tile * kTile + 16 * i, last_pos & ~15);
+    return (((int64_t)lane_of(p.page, base + i) * a.kv_heads + h) * a.B + (key & (a.B - 1))) * a.D;
+  }
+
+  // The bytes of this wave's 32 keys of a tile.
+  struct Bytes {
+    u32x4 k[2][DP / 64];
+    Vec<uint32_t, VB / 4> v[8];
+  };
+  static __device__ __forceinline__ Bytes load(const Args& a, const Pages& p, int base, int h, int tile, int last_pos) {
+    const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6, n = lane & 15, g = lane >> 4;
+    Bytes b;
+    int64_t at[2];
+#pragma unroll
+    for (int t = 0; t < 2; t++) {
+      at[t] = row_at(a, p, base, 2 * wave + t, h, tile, last_pos);
+      // behind element D - 1 the same key's first ones: q is zero there
+#pragma unroll
+      for (int j = 0; j < DP / 64; j++)
+        b.k[t][j] = ld16(a.k + at[t] + n * a.D + (j * 64 + g * 16 < a.D ? j * 64 + g * 16 : 0));
+    }
+    const int vd = n * VB < a.D ? n * VB : 0;
+#pragma unroll
+    for (int i = 0; i < 8; i++)
+      b.v[i] = *reinterpret_cast<const Vec<uint32_t, VB / 4>*>(a.v + at[i >> 2] + (4 * g + (i & 3)) * a.D + vd);
+    return b;
+  }
+
+  static __device__ __forceinline__ void run(const Args& a, const Seq& sq, const Task& task, int s, int h, int begin,
+                                             int end, int part, float* lds) {
+    const int tid = (int)threadIdx.x, lane = tid & 63, wave = tid >> 6, n = lane & 15, g = lane >> 4;
+    u32x4* const frags = reinterpret_cast<u32x4*>(lds);  // [32 keys][K, V][operand][lane]
+    int* const nan_word = reinterpret_cast<int*>(lds + kWaves * 2 * kFrags * 256);
+    const int32_t* table = a.table + s * a.table_row;
+    const int row0 = task.r0 + wave * 16 * R;
+
+    // ---- this wave's rows ----
+    u32x4 q[R][DP / 32];
+    f32x4 o[R][DP / 16];
+    float m[R], l[R];
+    int hi[R], lo[R];
+#pragma unroll
+    for (int r = 0; r < R; r++) {
+      const int row = row0 + r * 16 + n, tok = row / a.group;
+      const bool ok = row < task.r1;
+      hi[r] = ok ? sq.past + tok : 0x7fffffff;
+      lo[r] = ok && a.window > 0 ? hi[r] - a.window + 1 : (int)0x80000000;
+      const uint16_t* qp =
+          a.q + (ok ? (int64_t)(sq.c0 + tok) * a.q_token + (int64_t)(h * a.group + row - tok * a.group) * a.q_head : 0);
+#pragma unroll
+      for (int j = 0; j < DP / 32; j++) {
+        const int d = (j >> 1) * 64 + g * 16 + (j & 1) * 8;
+        u32x4 v = {0u, 0u, 0u, 0u};
+        if (ok && d < a.D) {
+          if (a.q_wide) {
+            v = ld16(qp + d);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; i++) v[i] = (uint32_t)qp[d + 2 * i] | (uint32_t)qp[d + 2 * i + 1] << 16;
+          }
+        }
+        q[r][j] = v;
+      }
+#pragma unroll
+      for (int j = 0; j < DP / 16; j++) o[r][j] = (f32x4){0.f, 0.f, 0.f, 0.f};
+      m[r] = -kInf;
+      l[r] = 0.f;
+    }
+    float vref = 0.f;
+    const int all_from = a.window > 0 ? max(task.last_pos - a.window + 1, 0) : 0;
+    const int any_from = a.window > 0 ? max(task.first_pos - a.window + 1, 0) : 0;
+
+    Pages pages = load_pages(a, table, h, begin, task.last_pos), next_pages = pages;
+    Bytes raw = load(a, pages, 0, h, begin, task.last_pos);
+    for (int tile = begin; tile < end; tile++) {
+      const int base = ((tile - begin) & 7) * kSubs;
+      const int key0 = tile * kTile;
+      const bool partial = key0 < all_from || key0 + kTile - 1 > task.first_pos;
+      meet();  // the last tile has been read
+      // ---- this wave's 32 keys into LDS ----
+      {
+        u32x4* kf = frags + (wave * 2) * kFrags * 64 + lane;
+        u32x4* vf = kf + kFrags * 64;
+        if (partial) {
+          bool has = false;
+#pragma unroll
+          for (int i = 0; i < 8; i++) {
+            const int key = key0 + wave * 32 + (i >> 2) * 16 + 4 * g + (i & 3);
+            const bool seen = key >= any_from && key <= task.last_pos;
+#pragma unroll
+            for (int w = 0; w < VB / 4; w++) {
+              const uint32_t v = seen ? raw.v[i].v[w] : 0u;
+              const uint32_t hit = ((v & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+              has |= hit != 0;
+              raw.v[i].v[w] = v & ~((hit >> 7) * 0xffu);
+            }
+          }
+          if (__ballot(has) && lane == 0) *nan_word = tile;
+        }
+#pragma unroll
+        for (int t = 0; t < 2; t++)
+#pragma unroll
+          for (int j = 0; j < DP / 64; j++) {
+            kf[(t * (DP / 32) + 2 * j) * 64] = widen8<BF16>(raw.k[t][j][0], raw.k[t][j][1]);
+            kf[(t * (DP / 32) + 2 * j + 1) * 64] = widen8<BF16>(raw.k[t][j][2], raw.k[t][j][3]);
+          }
+#pragma unroll
+        for (int w = 0; w < VB / 4; w++) {
+          uint32_t v[8];
+#pragma unroll
+          for (int i = 0; i < 8; i++) v[i] = raw.v[i].v[w];
+          u32x4 e[4];
+          zip4(v, e);
+#pragma unroll
+          for (int j = 0; j < 4; j++) vf[(4 * w + j) * 64] = e[j];
+        }
+      }
+      if (tile + 1 < end) {
+        if (((tile + 1 - begin) & 7) == 0) next_pages = load_pages(a, table, h, tile + 1, task.last_pos);
+        raw = load(a, next_pages, ((tile + 1 - begin) & 7) * kSubs, h, tile + 1, task.last_pos);
+      }
+      meet();  // the tile is there
+      const bool nan_v = partial && *nan_word == tile;
+
+      float ratio = 1.0f;
+      const float vmax = lane_of(pages.vmax, base);
+      if (vmax > vref) {
+        ratio = vref / vmax;
+        vref = vmax;
+      }
+      const float inv = vref > 0.f ? 1.0f / vref : 0.f;
+
+      for (int half = 0; half < 2; half++) {  // 64 keys
+        const int sub0 = base + half * 4, half0 = key0 + half * 64;
+        if (half0 > task.last_pos) break;
+        f32x4 sc[R][4];
+#pragma unroll
+        for (int t = 0; t < 4; t++) {
+          const u32x4* kf = frags + ((half * 2 + (t >> 1)) * 2) * kFrags * 64 + (t & 1) * (DP / 32) * 64 + lane;
+#pragma unroll
+          for (int r = 0; r < R; r++) sc[r][t] = (f32x4){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int j = 0; j < DP / 32; j++) {
+            const u32x4 k = kf[j * 64];
+#pragma unroll
+            for (int r = 0; r < R; r++) sc[r][t] = mma_dense<BF16>(k, q[r][j], sc[r][t]);
+          }
+        }
+        float ks[4], vs[4];
+#pragma unroll
+        for (int t = 0; t < 4; t++) {
+          ks[t] = lane_of(pages.ks, sub0 + t);
+          vs[t] = lane_of(pages.vs, sub0 + t) * inv;
+        }
+        u32x4 pr[R][2];
+#pragma unroll
+        for (int r = 0; r < R; r++) {
+          float mx = m[r];
+#pragma unroll
+          for (int t = 0; t < 4; t++)
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+              float p = sc[r][t][i] * ks[t];
+              if (partial) {
+                const int key = half0 + 16 * t + 4 * g + i;
+                if (key > hi[r] || key < lo[r] || key > task.last_pos) p = -kInf;
+              }
+              sc[r][t][i] = p;
+              mx = fmaxf(mx, p);
+            }
+          mx = fmaxf(mx, __shfl_xor(mx, 16));
+          mx = fmaxf(mx, __shfl_xor(mx, 32));
+          const float mu = finite_or_0(mx);
+          const float f = exp2_(m[r] - mu);
+          m[r] = mx;
+          const float off = mu - kBias;
+          float sum = 0.f;
+#pragma unroll
+          for (int u = 0; u < 2; u++) {
+            f16x8 ph;
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+              const float e = exp2_(sc[r][2 * u + (i >> 2)][i & 3] - off);
+              sum += e;
+              ph[i] = (_Float16)(e * vs[2 * u + (i >> 2)]);
+            }
+            pr[r][u] = __builtin_bit_cast(u32x4, ph);
+          }
+          l[r] = l[r] * f + sum;
+          const float fr = f * (half == 0 ? ratio : 1.0f);
+          if (__ballot(fr != 1.0f)) {
+#pragma unroll
+            for (int j = 0; j < DP / 16; j++) o[r][j] *= fr;
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < 2; u++) {
+          const u32x4* vf = frags + ((half * 2 + u) * 2 + 1) * kFrags * 64 + lane;
+#pragma unroll
+          for (int j = 0; j < DP / 16; j++) {
+            const u32x4 v = vf[j * 64];
+#pragma unroll
+            for (int r = 0; r < R; r++) o[r][j] = mma_dense<false>(v, pr[r][u], o[r][j]);
+          }
+        }
+        if (nan_v) {
+          // rare: V holds NaN in a row that not every row of the task sees (as in attention.hip)
+          const int vd = n * VB < a.D ? n * VB : 0;
+#pragma unroll 1
+          for (int u = 0; u < 2; u++) {
+            u32x4 see[R];
+            uint32_t nan[VB / 4][8];
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+              const int sub = half * 4 + u * 2 + (i >> 2), key = key0 + 16 * sub + 4 * g + (i & 3);
+              const uint32_t* v = reinterpret_cast<const uint32_t*>(
+                  a.v + row_at(a, pages, base, sub, h, tile, task.last_pos) + (4 * g + (i & 3)) * a.D + vd);
+              const bool seen = key >= any_from && key <= task.last_pos;
+#pragma unroll
+              for (int w = 0; w < VB / 4; w++) nan[w][i] = seen ? (((v[w] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7 : 0u;
+            }
+#pragma unroll
+            for (int r = 0; r < R; r++) {
+              f16x8 one;
+#pragma unroll
+              for (int i = 0; i < 8; i++) {
+                const int key = half0 + u * 32 + (i >> 2) * 16 + 4 * g + (i & 3);
+                one[i] = key <= hi[r] && key >= lo[r] && key <= task.last_pos ? (_Float16)1.0f : (_Float16)0.0f;
+              }
+              see[r] = __builtin_bit_cast(u32x4, one);
+            }
+#pragma unroll
+            for (int w = 0; w < VB / 4; w++) {
+              u32x4 e[4];
+              zip4(nan[w], e);
+#pragma unroll
+              for (int j = 0; j < 4; j++)
+#pragma unroll
+                for (int r = 0; r < R; r++) {
+                  const f32x4 hit = mma_dense<false>(e[j], see[r], (f32x4){0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+                  for (int i = 0; i < 4; i++)
+                    if (hit[i] > 0.f) o[r][4 * w + j][i] = __builtin_nanf("");
+                }
+            }
+          }
+        }
+      }
+      if (((tile + 1 - begin) & 7) == 0) pages = next_pages;
+    }
+
+    // ---- a lane holds elements 4g VB .. 4g VB + 4 VB - 1 of its row ----
+    float* slot = a.parts + (int64_t)part * (kRows * (DP + 2));
+    const __amdgpu_buffer_rsrc_t rs = rsrc(slot, kRows * (DP + 2) * 4);
+#pragma unroll
+    for (int r = 0; r < R; r++) {
+      l[r] += __shfl_xor(l[r], 16);
+      l[r] += __shfl_xor(l[r], 32);
+      const int row = wave * 16 * R + r * 16 + n;  // of the task
+      if (task.r0 + row >= task.r1) continue;
+      const float by = l[r] == 0.f ? 0.f : vref / l[r];
+      if (a.lse && g == 0 && part < 0) store_lse(a, sq, h, task.r0 + row, lse_of(m[r], l[r]));
+      if (part >= 0 && g == 0) {
+        const u32x2 ml = {__float_as_uint(m[r]), __float_as_uint(l[r])};
+        __builtin_amdgcn_raw_buffer_store_b64(ml, rs, (kRows * DP + 2 * row) * 4, 0, kCoherent);
+      }
+#pragma unroll
+      for (int e = 0; e < 4 * VB; e += 8) {
+        const int d = 4 * g * VB + e;
+        if (d >= a.D) continue;
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; i++) v[i] = o[r][(e + i) % VB][(e + i) / VB] * by;
+        if (part < 0) {
+          store8<BF16>(a, out_at(a, sq, h, task.r0 + row, d), v);
+        } else {
+          const f32x4 v0 = {v[0], v[1], v[2], v[3]}, v1 = {v[4], v[5], v[6], v[7]};
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v0), rs, (row * DP + d) * 4, 0, kCoherent);
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v1), rs, (row * DP + d + 4) * 4, 0, kCoherent);
+        }
+      }
+    }
+  }
+};
+
+}  // namespace
+
+uint64_t attention_chunk_workspace_bytes(int64_t dim) {
+  return dim <= 64 ? workspace_bytes<Chunk<true, 64, 2>>() : workspace_bytes<Chunk<true, 128, 2>>();
+}
+
+hipError_t launch_attention_chunk(bool bf16, Args& a, void* ws, uint64_t ws_bytes, hipStream_t s) {
+  if (a.D <= 64) return bf16 ? go<Chunk<true, 64, 2>>(a, ws, ws_bytes, s) : go<Chunk<false, 64, 2>>(a, ws, ws_bytes, s);
+  return bf16 ? go<Chunk<true, 128, 2>>(a, ws, ws_bytes, s) : go<Chunk<false, 128, 2>>(a, ws, ws_bytes, s);
+}
+
+}  // namespace patch
