@@ -101,16 +101,18 @@ __device__ __forceinline__ Bytes<DP> load_step(const Args& a, const Pages& p, in
     b.vp[t] = a.v + at;
     b.ks[t] = lane_of(p.ks[t], i);
     b.vs[t] = lane_of(p.vs[t], i);
-    const uint8_t* kp = a.k + at + n * a.D;
+    const uint8_t* kp = a.k + at;
     // Behind element D - 1 the same key's first ones: q is zero there (and a
     // NaN among them would make the score NaN in any case).
 #pragma unroll
-    for (int j = 0; j < DP / 64; j++) b.k[t][j] = ld16(kp + (j * 64 + g * 16 < a.D ? j * 64 + g * 16 : 0));
+    for (int j = 0; j < DP / 64; j++)
+      b.k[t][j] = ld16(kp + (uint32_t)(n * a.D + (j * 64 + g * 16 < a.D ? j * 64 + g * 16 : 0)));
   }
-  const int vd = n * VB < a.D ? n * VB : 0;  // likewise; those outputs are not stored
+  // likewise; those outputs are not stored
+  const uint32_t vo = (uint32_t)(4 * g * a.D + (n * VB < a.D ? n * VB : 0));
 #pragma unroll
   for (int i8 = 0; i8 < 8; i8++)
-    b.v[i8] = *reinterpret_cast<const Vec<uint32_t, VB / 4>*>(b.vp[i8 >> 2] + (4 * g + (i8 & 3)) * a.D + vd);
+    b.v[i8] = *reinterpret_cast<const Vec<uint32_t, VB / 4>*>(b.vp[i8 >> 2] + (i8 & 3) * a.D + vo);
   return b;
 }
 
@@ -146,7 +148,7 @@ __device__ __forceinline__ void start_rows(const Args& a, const Seq& sq, const T
           for (int i = 0; i < 4; i++) v[i] = (uint32_t)qp[d + 2 * i] | (uint32_t)qp[d + 2 * i + 1] << 16;
         }
       }
-      x.q[r][j] = v;
+      x.q[r][j] = v ^ a.q_flip;
     }
 #pragma unroll
     for (int j = 0; j < DP / 16; j++) x.o[r][j] = (f32x4){0.f, 0.f, 0.f, 0.f};
@@ -226,8 +228,7 @@ __device__ __forceinline__ void do_step(const Args& a, const Task& task, int ste
       }
       mx = fmaxf(mx, p[i]);
     }
-    mx = fmaxf(mx, __shfl_xor(mx, 16));
-    mx = fmaxf(mx, __shfl_xor(mx, 32));
+    mx = quad_max(mx);
     const float mu = finite_or_0(mx);
     const float f = exp2_(x.m[r] - mu);
     x.m[r] = mx;
@@ -334,9 +335,7 @@ struct Few {
   float* lml = lds + kWaves * kRows * kLd;  // [wave][row][m, l], then [wave] vref
 #pragma unroll
   for (int r = 0; r < R; r++) {
-    // the lanes of a row hold parts of its sum
-    x.l[r] += __shfl_xor(x.l[r], 16);
-    x.l[r] += __shfl_xor(x.l[r], 32);
+    x.l[r] = quad_sum(x.l[r]);  // the lanes of a row hold parts of its sum
     float* at = lds + (wave * kRows + r * 16 + n) * kLd + 4 * g * VB;
 #pragma unroll
     for (int i = 0; i < 4; i++)
@@ -467,7 +466,8 @@ hipError_t launch_attention(const patch_attention_args& p, const patch_kv_cache&
   a.pages = (int)c.pages;
   a.max_pages = (int)p.max_pages;
   a.window = (int)std::min<int64_t>(p.window, 0x3fffffff);
-  a.scale = (float)p.scale * kLog2e;
+  a.scale = fabsf((float)p.scale * kLog2e);
+  a.q_flip = p.scale < 0 ? 0x80008000u : 0u;
   a.q_wide = ((p.q_token | p.q_head) & 7) == 0 && ((uintptr_t)p.q_dev & 15) == 0;
   a.o_wide = ((p.out_token | p.out_head) & 7) == 0 && ((uintptr_t)p.out_dev & 15) == 0;
   a.out_f32 = p.out_dtype == PATCH_F32;

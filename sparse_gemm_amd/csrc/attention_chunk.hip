@@ -19,6 +19,7 @@ using namespace attn;
 namespace {
 
 constexpr int kTile = 128;           // keys of a tile (a step of the line)
+constexpr float kNoScale = -200.0f;  // log2 of a scale that is 0
 constexpr int kSubs = kTile / 16;    // its sub-tiles of 16 keys, each in one page
 
 // Waits for this wave's LDS traffic, not for loads from memory, and meets the others.
@@ -36,7 +37,7 @@ struct Chunk {
   // Pages of eight tiles, a sub-tile a lane.
   struct Pages {
     int page;
-    float ks, vs, vmax;  // vmax: the largest |v scale| of the lane's tile
+    float ks, vs, vmax;  // vs: log2 of the v scale, vmax: the largest of the lane's tile
   };
   static __device__ __forceinline__ Pages load_pages(const Args& a, const int32_t* table, int h, int tile, int last_pos) {
     Pages p;
@@ -46,8 +47,9 @@ struct Chunk {
     p.page = ok ? page : 0;
     const int64_t at = (int64_t)p.page * a.kv_heads + h;
     p.ks = ok ? a.ks[at] * a.scale : __builtin_nanf("");
-    p.vs = ok ? a.vs[at] : 0.f;
-    p.vmax = fabsf(p.vs);
+    // a scale of 0 (or a page outside the cache) counts as a very small one
+    p.vs = fmaxf(ok ? __log2f(a.vs[at]) : kNoScale, kNoScale);
+    p.vmax = p.vs;
 #pragma unroll
     for (int d = 1; d < kSubs; d *= 2) p.vmax = fmaxf(p.vmax, __shfl_xor(p.vmax, d));
     return p;
@@ -65,21 +67,22 @@ struct Chunk {
     Vec<uint32_t, VB / 4> v[8];
   };
   static __device__ __forceinline__ Bytes load(const Args& a, const Pages& p, int base, int h, int tile, int last_pos) {
-    const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6, n = lane & 15, g = lane >> 4;
+    const int lane = (int)threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), n = lane & 15,
+              g = lane >> 4;
     Bytes b;
-    int64_t at[2];
+    // uniform addresses, and a lane's 32-bit offset from them; behind element D
+    // - 1 the same key's first ones: q is zero there
+    const uint32_t vo = (uint32_t)(4 * g * a.D + (n * VB < a.D ? n * VB : 0));
 #pragma unroll
     for (int t = 0; t < 2; t++) {
-      at[t] = row_at(a, p, base, 2 * wave + t, h, tile, last_pos);
-      // behind element D - 1 the same key's first ones: q is zero there
+      const int64_t at = row_at(a, p, base, 2 * wave + t, h, tile, last_pos);
 #pragma unroll
       for (int j = 0; j < DP / 64; j++)
-        b.k[t][j] = ld16(a.k + at[t] + n * a.D + (j * 64 + g * 16 < a.D ? j * 64 + g * 16 : 0));
-    }
-    const int vd = n * VB < a.D ? n * VB : 0;
+        b.k[t][j] = ld16(a.k + at + (uint32_t)(n * a.D + (j * 64 + g * 16 < a.D ? j * 64 + g * 16 : 0)));
 #pragma unroll
-    for (int i = 0; i < 8; i++)
-      b.v[i] = *reinterpret_cast<const Vec<uint32_t, VB / 4>*>(a.v + at[i >> 2] + (4 * g + (i & 3)) * a.D + vd);
+      for (int i = 0; i < 4; i++)
+        b.v[4 * t + i] = *reinterpret_cast<const Vec<uint32_t, VB / 4>*>(a.v + at + i * a.D + vo);
+    }
     return b;
   }
 
@@ -116,14 +119,14 @@ struct Chunk {
             for (int i = 0; i < 4; i++) v[i] = (uint32_t)qp[d + 2 * i] | (uint32_t)qp[d + 2 * i + 1] << 16;
           }
         }
-        q[r][j] = v;
+        q[r][j] = v ^ a.q_flip;
       }
 #pragma unroll
       for (int j = 0; j < DP / 16; j++) o[r][j] = (f32x4){0.f, 0.f, 0.f, 0.f};
       m[r] = -kInf;
       l[r] = 0.f;
     }
-    float vref = 0.f;
+    float vref = -kInf;  // log2 of what o is in units of: the largest v scale so far
     const int all_from = a.window > 0 ? max(task.last_pos - a.window + 1, 0) : 0;
     const int any_from = a.window > 0 ? max(task.first_pos - a.window + 1, 0) : 0;
 
@@ -179,13 +182,12 @@ struct Chunk {
       meet();  // the tile is there
       const bool nan_v = partial && *nan_word == tile;
 
-      float ratio = 1.0f;
       const float vmax = lane_of(pages.vmax, base);
+      float ratio = 1.0f;
       if (vmax > vref) {
-        ratio = vref / vmax;
+        ratio = exp2_(vref - vmax);
         vref = vmax;
       }
-      const float inv = vref > 0.f ? 1.0f / vref : 0.f;
 
       for (int half = 0; half < 2; half++) {  // 64 keys
         const int sub0 = base + half * 4, half0 = key0 + half * 64;
@@ -203,11 +205,31 @@ struct Chunk {
             for (int r = 0; r < R; r++) sc[r][t] = mma_dense<BF16>(k, q[r][j], sc[r][t]);
           }
         }
-        float ks[4], vs[4];
+        // probabilities times the v scale (relative to vref): 2^(s + log2(vs) - m
+        // + kBias), one multiply-add and the exponential; the sum takes them
+        // divided by it again
+        float ks[4], lv[4], vi[4];
 #pragma unroll
         for (int t = 0; t < 4; t++) {
           ks[t] = lane_of(pages.ks, sub0 + t);
-          vs[t] = lane_of(pages.vs, sub0 + t) * inv;
+          const float v = lane_of(pages.vs, sub0 + t) - vref;
+          lv[t] = fmaxf(v, -100.0f);
+          vi[t] = exp2_(-lv[t]);
+          lv[t] += kBias;
+        }
+        if (partial) {
+#pragma unroll
+          for (int t = 0; t < 4; t++) {
+#pragma unroll
+            for (int r = 0; r < R; r++)
+#pragma unroll
+              for (int i = 0; i < 4; i++) {
+                const int key = half0 + 16 * t + 4 * g + i;
+                const bool seen = key <= hi[r] && key >= lo[r] && key <= task.last_pos;
+                sc[r][t][i] = seen ? sc[r][t][i] * ks[t] : -kInf;
+              }
+            ks[t] = 1.0f;
+          }
         }
         u32x4 pr[R][2];
 #pragma unroll
@@ -215,35 +237,29 @@ struct Chunk {
           float mx = m[r];
 #pragma unroll
           for (int t = 0; t < 4; t++)
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-              float p = sc[r][t][i] * ks[t];
-              if (partial) {
-                const int key = half0 + 16 * t + 4 * g + i;
-                if (key > hi[r] || key < lo[r] || key > task.last_pos) p = -kInf;
-              }
-              sc[r][t][i] = p;
-              mx = fmaxf(mx, p);
-            }
-          mx = fmaxf(mx, __shfl_xor(mx, 16));
-          mx = fmaxf(mx, __shfl_xor(mx, 32));
+            mx = fmaxf(mx, fmaxf(fmaxf(sc[r][t][0], sc[r][t][1]), fmaxf(sc[r][t][2], sc[r][t][3])) * ks[t]);
+          mx = quad_max(mx);
           const float mu = finite_or_0(mx);
           const float f = exp2_(m[r] - mu);
           m[r] = mx;
-          const float off = mu - kBias;
-          float sum = 0.f;
+          l[r] *= f;
 #pragma unroll
           for (int u = 0; u < 2; u++) {
             f16x8 ph;
 #pragma unroll
-            for (int i = 0; i < 8; i++) {
-              const float e = exp2_(sc[r][2 * u + (i >> 2)][i & 3] - off);
-              sum += e;
-              ph[i] = (_Float16)(e * vs[2 * u + (i >> 2)]);
+            for (int t = 0; t < 2; t++) {
+              const float off = lv[2 * u + t] - mu;
+              float sum = 0.f;
+#pragma unroll
+              for (int i = 0; i < 4; i++) {
+                const float e = exp2_(fmaf(sc[r][2 * u + t][i], ks[2 * u + t], off));
+                sum += e;
+                ph[4 * t + i] = (_Float16)e;
+              }
+              l[r] = fmaf(sum, vi[2 * u + t], l[r]);
             }
             pr[r][u] = __builtin_bit_cast(u32x4, ph);
           }
-          l[r] = l[r] * f + sum;
           const float fr = f * (half == 0 ? ratio : 1.0f);
           if (__ballot(fr != 1.0f)) {
 #pragma unroll
@@ -311,11 +327,10 @@ struct Chunk {
     const __amdgpu_buffer_rsrc_t rs = rsrc(slot, kRows * (DP + 2) * 4);
 #pragma unroll
     for (int r = 0; r < R; r++) {
-      l[r] += __shfl_xor(l[r], 16);
-      l[r] += __shfl_xor(l[r], 32);
+      l[r] = quad_sum(l[r]);
       const int row = wave * 16 * R + r * 16 + n;  // of the task
       if (task.r0 + row >= task.r1) continue;
-      const float by = l[r] == 0.f ? 0.f : vref / l[r];
+      const float by = l[r] == 0.f || vref <= kNoScale ? 0.f : exp2_(vref) / l[r];
       if (a.lse && g == 0 && part < 0) store_lse(a, sq, h, task.r0 + row, lse_of(m[r], l[r]));
       if (part >= 0 && g == 0) {
         const u32x2 ml = {__float_as_uint(m[r]), __float_as_uint(l[r])};

@@ -41,6 +41,7 @@ struct Args {
   int64_t q_token, q_head, o_token, o_head, table_row;
   int T, S, heads, kv_heads, group, D, B, shift, pages, max_pages, window;
   float scale;  // with log2(e)
+  uint32_t q_flip;  // sign bits: of a negative scale, which the rows of q take
   bool q_wide, o_wide, out_f32;
 };
 
@@ -63,6 +64,28 @@ __device__ __forceinline__ uint32_t widen2(uint32_t w) {
 template <bool BF16>
 __device__ __forceinline__ u32x4 widen8(uint32_t lo, uint32_t hi) {
   return (u32x4){widen2<BF16, false>(lo), widen2<BF16, true>(lo), widen2<BF16, false>(hi), widen2<BF16, true>(hi)};
+}
+
+// The largest of a row's four lanes (16 apart), and their sum.  A swap of two
+// copies' rows of 16 (halves of 32) leaves each lane both values.
+__device__ __forceinline__ void swapped(float x, float& a, float& b, bool by32) {
+  const uint32_t u = __float_as_uint(x);
+  const auto r = by32 ? __builtin_amdgcn_permlane32_swap(u, u, false, false)
+                      : __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  a = __uint_as_float(r[0]);
+  b = __uint_as_float(r[1]);
+}
+__device__ __forceinline__ float quad_max(float x) {
+  float a, b;
+  swapped(x, a, b, false);
+  swapped(fmaxf(a, b), a, b, true);
+  return fmaxf(a, b);
+}
+__device__ __forceinline__ float quad_sum(float x) {
+  float a, b;
+  swapped(x, a, b, false);
+  swapped(a + b, a, b, true);
+  return a + b;
 }
 
 // Four neighbouring elements of 8 keys (a word a key) as four A operands of
@@ -336,62 +359,59 @@ __global__ __launch_bounds__(kThreads, Body::kPerCu) void k_attention_line(Args 
   __shared__ int wave_sum[kWaves];
   __shared__ int joined;
   constexpr int kTaskCost = Body::kTaskCost;
+  const int lane = (int)threadIdx.x & 63;
   Seq mine{0, 0, 0, false};  // of this lane's sequence
-  if constexpr (!MANY) {
-    const int lane = (int)threadIdx.x & 63;
-    if (lane < a.S) mine = seq_of(a, lane);
-    const LaneLine pieces(lane < a.S ? pieces_of<Body>(a, mine) * a.kv_heads : 0);
-    if (pieces.total <= (int)gridDim.x) {
-      if ((int)blockIdx.x >= pieces.total) return;
-      const Place pl = pieces.find((int)blockIdx.x);
-      const Seq sq{lane_of(mine.c0, pl.s), lane_of(mine.n, pl.s), lane_of(mine.past, pl.s), lane_of((int)mine.bad, pl.s) != 0};
-      const int per_head = (pl.to - pl.from) / a.kv_heads, h = ((int)blockIdx.x - pl.from) / per_head;
-      int w0 = pl.from + h * per_head, rt = 0;
-      Task task = task_of<Body>(a, sq, 0);
-      int count = pieces_of<Body>(task);
-      while (w0 + count <= (int)blockIdx.x) {
-        w0 += count;
-        task = task_of<Body>(a, sq, ++rt);
-        count = pieces_of<Body>(task);
-      }
-      const int i = (int)blockIdx.x - w0, steps = task.end - task.begin;
-      const int each = steps / count, more = steps - each * count;  // the first `more` pieces have one step more
-      const int begin = task.begin + i * each + min(i, more);
-      run_piece<Body>(a, sq, task, pl.s, h, begin, begin + each + (i < more ? 1 : 0), w0, count, lds, &joined);
-      return;
-    }
-  }
-  const auto line = [&] {
+  if (!MANY && lane < a.S) mine = seq_of(a, lane);
+  const auto seq_at = [&](int s) {
+    return MANY ? seq_of(a, s)
+                : Seq{lane_of(mine.c0, s), lane_of(mine.n, s), lane_of(mine.past, s), lane_of((int)mine.bad, s) != 0};
+  };
+  const auto make = [&](auto f) {  // a line of f(sequence) for every head
     if constexpr (MANY)
       return LdsLine(a.S, reinterpret_cast<int*>(lds + Body::kLds), wave_sum,
-                     [&](int s) { return cost_of<Body>(a, seq_of(a, s)) * a.kv_heads; });
+                     [&](int s) { return f(seq_of(a, s)) * a.kv_heads; });
     else
-      return LaneLine(((int)threadIdx.x & 63) < a.S ? cost_of<Body>(a, mine) * a.kv_heads : 0);
-  }();
-  const int per = (line.total + (int)gridDim.x - 1) / (int)gridDim.x;
+      return LaneLine(lane < a.S ? f(mine) * a.kv_heads : 0);
+  };
+  auto line = make([&](const Seq& q) { return pieces_of<Body>(a, q); });
+  const bool even = line.total <= (int)gridDim.x;  // a piece a workgroup
+  if (!even) line = make([&](const Seq& q) { return cost_of<Body>(a, q); });
+  const int per = even ? 1 : (line.total + (int)gridDim.x - 1) / (int)gridDim.x;
   int u = per * (int)blockIdx.x;
   const int u_end = min(u + per, line.total);
   while (u < u_end) {
     const Place pl = line.find(u);
-    const Seq sq = MANY ? seq_of(a, pl.s)
-                        : Seq{lane_of(mine.c0, pl.s), lane_of(mine.n, pl.s), lane_of(mine.past, pl.s),
-                              lane_of((int)mine.bad, pl.s) != 0};
+    const Seq sq = seq_at(pl.s);
     const int per_head = (pl.to - pl.from) / a.kv_heads, h = (u - pl.from) / per_head;
     int at = pl.from + h * per_head, rt = 0;  // where the task begins on the line
     Task task = task_of<Body>(a, sq, 0);
-    while (at + (task.end - task.begin) + kTaskCost <= u) {
-      at += task.end - task.begin + kTaskCost;
+    int size = even ? pieces_of<Body>(task) : task.end - task.begin + kTaskCost;
+    while (at + size <= u) {
+      at += size;
       task = task_of<Body>(a, sq, ++rt);
+      size = even ? pieces_of<Body>(task) : task.end - task.begin + kTaskCost;
     }
-    at += kTaskCost;  // its first step
-    const int task_end = at + (task.end - task.begin), from = max(u, at), to = min(u_end, task_end);
-    if (from < to) {
-      const int w0 = at / per;
-      run_piece<Body>(a, sq, task, pl.s, h, task.begin + from - at, task.begin + to - at, w0,
-                             (task_end - 1) / per - w0 + 1, lds, &joined);
+    int begin, end, w0, count;
+    if (even) {
+      const int steps = task.end - task.begin, i = u - at;
+      const int each = steps / size, more = steps - each * size;  // the first `more` pieces have one step more
+      begin = task.begin + i * each + min(i, more);
+      end = begin + each + (i < more ? 1 : 0);
+      w0 = at;
+      count = size;
+      u = u_end;
+    } else {
+      const int first = at + kTaskCost, last = at + size;  // the task's steps on the line
+      begin = task.begin + max(u - first, 0);
+      end = task.begin + min(u_end, last) - first;
+      w0 = first / per;
+      count = (last - 1) / per - w0 + 1;
+      u = last;
+    }
+    if (begin < end) {
+      run_piece<Body>(a, sq, task, pl.s, h, begin, end, w0, count, lds, &joined);
       __syncthreads();  // LDS is used again
     }
-    u = task_end;
   }
 }
 
