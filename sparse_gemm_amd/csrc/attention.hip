@@ -28,8 +28,7 @@
 // % 16) * DP / 16 + j.
 //
 // 8-bit values become 16-bit ones exactly (q's type for the scores; fp16 for
-// the second product, whose probabilities keep 11 bits: 2^(s - m + 14), up to
-// 16384, so that small ones do not fall under fp16's normal range).  A block's
+// the second product, whose probabilities keep 11 bits).  A block's
 // k scale multiplies the scores, its v scale the probabilities, relative to
 // the largest v scale so far (vref), o being kept in units of it.
 //
@@ -186,13 +185,14 @@ __device__ __forceinline__ void do_step(const Args& a, const Task& task, int ste
   }
   bool nan_v = false;
   if (partial) {
+    const int from = seldom(key0);
     // V rows that no row of the task sees hold anything at all: take zeros.  A
     // NaN in a row that some see must not reach the others through 0 * NaN: it
     // is taken out here and put back below, row by row.
     bool has = false;
 #pragma unroll
     for (int i = 0; i < 8; i++) {
-      const int key = key0 + (i >> 2) * 16 + 4 * g + (i & 3);
+      const int key = from + (i >> 2) * 16 + 4 * g + (i & 3);
       const bool seen = key >= any_from && key <= task.last_pos;
 #pragma unroll
       for (int w = 0; w < VB / 4; w++) {
@@ -206,11 +206,14 @@ __device__ __forceinline__ void do_step(const Args& a, const Task& task, int ste
     nan_v = __ballot(has) != 0;
   }
 
-  float ratio = 1.0f;
   const float vmax = fmaxf(fabsf(b.vs[0]), fabsf(b.vs[1]));
   if (vmax > x.vref) {
-    ratio = x.vref / vmax;
+    const float f = x.vref / vmax;
     x.vref = vmax;
+#pragma unroll
+    for (int r = 0; r < R; r++)
+#pragma unroll
+      for (int j = 0; j < DP / 16; j++) x.o[r][j] *= f;
   }
   const float inv = x.vref > 0.f ? 1.0f / x.vref : 0.f;
   const float vf[2] = {b.vs[0] * inv, b.vs[1] * inv};
@@ -218,34 +221,38 @@ __device__ __forceinline__ void do_step(const Args& a, const Task& task, int ste
 #pragma unroll
   for (int r = 0; r < R; r++) {
     float p[8];
-    float mx = x.m[r];
+    float mx = -kInf;
 #pragma unroll
-    for (int i = 0; i < 8; i++) {
-      p[i] = sc[r][i >> 2][i & 3] * b.ks[i >> 2];
-      if (partial) {
-        const int key = key0 + (i >> 2) * 16 + 4 * g + (i & 3);
+    for (int i = 0; i < 8; i++) p[i] = sc[r][i >> 2][i & 3] * b.ks[i >> 2];
+    if (partial) {
+      const int from = seldom(key0);
+#pragma unroll
+      for (int i = 0; i < 8; i++) {
+        const int key = from + (i >> 2) * 16 + 4 * g + (i & 3);
         if (key > x.hi[r] || key < x.lo[r] || key > task.last_pos) p[i] = -kInf;
       }
-      mx = fmaxf(mx, p[i]);
     }
-    mx = quad_max(mx);
-    const float mu = finite_or_0(mx);
-    const float f = exp2_(x.m[r] - mu);
-    x.m[r] = mx;
+#pragma unroll
+    for (int i = 0; i < 8; i++) mx = fmaxf(mx, p[i]);
+    if (__ballot(mx > x.m[r] + kSlack)) {
+      mx = fmaxf(x.m[r], quad_max(mx));
+      const float f = exp2_(x.m[r] - finite_or_0(mx));
+      x.m[r] = mx;
+      x.l[r] *= f;
+#pragma unroll
+      for (int j = 0; j < DP / 16; j++) x.o[r][j] *= f;
+    }
+    const float off = finite_or_0(x.m[r]) - kBias;
     float sum = 0.f;
     f16x8 ph;
 #pragma unroll
     for (int i = 0; i < 8; i++) {
-      const float e = exp2_(p[i] - (mu - kBias));
+      const float e = exp2_(p[i] - off);
       sum += e;
       ph[i] = (_Float16)(e * vf[i >> 2]);
     }
     pr[r] = __builtin_bit_cast(u32x4, ph);
-    x.l[r] = x.l[r] * f + sum;
-    if (__ballot(f * ratio != 1.0f)) {
-#pragma unroll
-      for (int j = 0; j < DP / 16; j++) x.o[r][j] *= f * ratio;
-    }
+    x.l[r] += sum;
   }
 
 #pragma unroll

@@ -142,10 +142,11 @@ struct Chunk {
         u32x4* kf = frags + (wave * 2) * kFrags * 64 + lane;
         u32x4* vf = kf + kFrags * 64;
         if (partial) {
+          const int from = seldom(key0);
           bool has = false;
 #pragma unroll
           for (int i = 0; i < 8; i++) {
-            const int key = key0 + wave * 32 + (i >> 2) * 16 + 4 * g + (i & 3);
+            const int key = from + wave * 32 + (i >> 2) * 16 + 4 * g + (i & 3);
             const bool seen = key >= any_from && key <= task.last_pos;
 #pragma unroll
             for (int w = 0; w < VB / 4; w++) {
@@ -183,10 +184,13 @@ struct Chunk {
       const bool nan_v = partial && *nan_word == tile;
 
       const float vmax = lane_of(pages.vmax, base);
-      float ratio = 1.0f;
       if (vmax > vref) {
-        ratio = exp2_(vref - vmax);
+        const float f = exp2_(vref - vmax);
         vref = vmax;
+#pragma unroll
+        for (int r = 0; r < R; r++)
+#pragma unroll
+          for (int j = 0; j < DP / 16; j++) o[r][j] *= f;
       }
 
       for (int half = 0; half < 2; half++) {  // 64 keys
@@ -194,16 +198,19 @@ struct Chunk {
         if (half0 > task.last_pos) break;
         f32x4 sc[R][4];
 #pragma unroll
-        for (int t = 0; t < 4; t++) {
-          const u32x4* kf = frags + ((half * 2 + (t >> 1)) * 2) * kFrags * 64 + (t & 1) * (DP / 32) * 64 + lane;
+        for (int t = 0; t < 4; t++)
 #pragma unroll
           for (int r = 0; r < R; r++) sc[r][t] = (f32x4){0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int j = 0; j < DP / 32; j++) {
-            const u32x4 k = kf[j * 64];
+        for (int j = 0; j < DP / 32; j++) {
+          u32x4 k[4];
 #pragma unroll
-            for (int r = 0; r < R; r++) sc[r][t] = mma_dense<BF16>(k, q[r][j], sc[r][t]);
-          }
+          for (int t = 0; t < 4; t++)
+            k[t] = frags[((half * 2 + (t >> 1)) * 2) * kFrags * 64 + ((t & 1) * (DP / 32) + j) * 64 + lane];
+#pragma unroll
+          for (int t = 0; t < 4; t++)
+#pragma unroll
+            for (int r = 0; r < R; r++) sc[r][t] = mma_dense<BF16>(k[t], q[r][j], sc[r][t]);
         }
         // probabilities times the v scale (relative to vref): 2^(s + log2(vs) - m
         // + kBias), one multiply-add and the exponential; the sum takes them
@@ -218,13 +225,14 @@ struct Chunk {
           lv[t] += kBias;
         }
         if (partial) {
+          const int from = seldom(half0);
 #pragma unroll
           for (int t = 0; t < 4; t++) {
 #pragma unroll
             for (int r = 0; r < R; r++)
 #pragma unroll
               for (int i = 0; i < 4; i++) {
-                const int key = half0 + 16 * t + 4 * g + i;
+                const int key = from + 16 * t + 4 * g + i;
                 const bool seen = key <= hi[r] && key >= lo[r] && key <= task.last_pos;
                 sc[r][t][i] = seen ? sc[r][t][i] * ks[t] : -kInf;
               }
@@ -234,15 +242,19 @@ struct Chunk {
         u32x4 pr[R][2];
 #pragma unroll
         for (int r = 0; r < R; r++) {
-          float mx = m[r];
+          float mx = -kInf;
 #pragma unroll
           for (int t = 0; t < 4; t++)
             mx = fmaxf(mx, fmaxf(fmaxf(sc[r][t][0], sc[r][t][1]), fmaxf(sc[r][t][2], sc[r][t][3])) * ks[t]);
-          mx = quad_max(mx);
-          const float mu = finite_or_0(mx);
-          const float f = exp2_(m[r] - mu);
-          m[r] = mx;
-          l[r] *= f;
+          if (__ballot(mx > m[r] + kSlack)) {
+            mx = fmaxf(m[r], quad_max(mx));
+            const float f = exp2_(m[r] - finite_or_0(mx));
+            m[r] = mx;
+            l[r] *= f;
+#pragma unroll
+            for (int j = 0; j < DP / 16; j++) o[r][j] *= f;
+          }
+          const float mu = finite_or_0(m[r]);
 #pragma unroll
           for (int u = 0; u < 2; u++) {
             f16x8 ph;
@@ -259,11 +271,6 @@ struct Chunk {
               l[r] = fmaf(sum, vi[2 * u + t], l[r]);
             }
             pr[r][u] = __builtin_bit_cast(u32x4, ph);
-          }
-          const float fr = f * (half == 0 ? ratio : 1.0f);
-          if (__ballot(fr != 1.0f)) {
-#pragma unroll
-            for (int j = 0; j < DP / 16; j++) o[r][j] *= fr;
           }
         }
 #pragma unroll

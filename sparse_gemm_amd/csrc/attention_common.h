@@ -23,7 +23,10 @@ namespace attn {
 
 constexpr int kWaves = 4;
 constexpr int kThreads = 64 * kWaves;
-constexpr float kBias = 14.0f;  // probabilities are 2^(s - m + kBias)
+// Probabilities are 2^(s - m + kBias), m being within kSlack of the running
+// maximum: sums and outputs are only scaled anew when it grows by more.  2^14
+// at most, and 2^-20 of the maximum still in fp16's normal range.
+constexpr float kBias = 6.0f, kSlack = 8.0f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kInf = __builtin_inff();
@@ -64,6 +67,13 @@ __device__ __forceinline__ uint32_t widen2(uint32_t w) {
 template <bool BF16>
 __device__ __forceinline__ u32x4 widen8(uint32_t lo, uint32_t hi) {
   return (u32x4){widen2<BF16, false>(lo), widen2<BF16, true>(lo), widen2<BF16, false>(hi), widen2<BF16, true>(hi)};
+}
+
+// A value for use in a block that seldom runs: what is computed from it stays
+// in the block (the compiler would rather compute it every time and select).
+__device__ __forceinline__ int seldom(int x) {
+  asm volatile("" : "+s"(x));
+  return x;
 }
 
 // The largest of a row's four lanes (16 apart), and their sum.  A swap of two
