@@ -25,7 +25,8 @@ constexpr int kSubs = kTile / 16;    // its sub-tiles of 16 keys, each in one pa
 // Waits for this wave's LDS traffic, not for loads from memory, and meets the others.
 __device__ __forceinline__ void meet() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
-template <bool BF16, int DP, int R>
+// FULL: dim is DP, and a row's distance a constant.
+template <bool BF16, int DP, int R, bool FULL>
 struct Chunk {
   static constexpr bool kBf16 = BF16;
   static constexpr int kDim = DP, kRows = kWaves * 16 * R, kStep = kTile, kMinSteps = 4, kTaskCost = 2;
@@ -36,52 +37,59 @@ struct Chunk {
 
   // Pages of eight tiles, a sub-tile a lane.
   struct Pages {
-    int page;
-    float ks, vs, vmax;  // vs: log2 of the v scale, vmax: the largest of the lane's tile
+    int64_t at;        // where the sub-tile's rows begin in k and v
+    float ks, vs;      // k scale (with the softmax's), log2 of the v scale
+    float vmax;        // the largest vs of the lane's tile
+    float lv, vi;      // vs relative to vref with kBias, and 2^ of minus the former
   };
   static __device__ __forceinline__ Pages load_pages(const Args& a, const int32_t* table, int h, int tile, int last_pos) {
     Pages p;
-    const int64_t key = min((int64_t)tile * kTile + 16 * (int64_t)(threadIdx.x & 63), (int64_t)(last_pos & ~15));
+    const int key = (int)min((int64_t)tile * kTile + 16 * (int64_t)(threadIdx.x & 63), (int64_t)(last_pos & ~15));
     const int page = table[key >> a.shift];
     const bool ok = page >= 0 && page < a.pages;
-    p.page = ok ? page : 0;
-    const int64_t at = (int64_t)p.page * a.kv_heads + h;
-    p.ks = ok ? a.ks[at] * a.scale : __builtin_nanf("");
+    const int64_t block = (int64_t)(ok ? page : 0) * a.kv_heads + h;
+    p.at = (block * a.B + (key & (a.B - 1))) * a.D;
+    p.ks = ok ? a.ks[block] * a.scale : __builtin_nanf("");
     // a scale of 0 (or a page outside the cache) counts as a very small one
-    p.vs = fmaxf(ok ? __log2f(a.vs[at]) : kNoScale, kNoScale);
+    p.vs = fmaxf(ok ? __log2f(a.vs[block]) : kNoScale, kNoScale);
     p.vmax = p.vs;
 #pragma unroll
     for (int d = 1; d < kSubs; d *= 2) p.vmax = fmaxf(p.vmax, __shfl_xor(p.vmax, d));
+    p.lv = p.vi = 0.f;
     return p;
   }
-  // Where sub-tile i's (of the tile's 8) first row lies.
-  static __device__ __forceinline__ int64_t row_at(const Args& a, const Pages& p, int base, int i, int h, int tile,
-                                                   int last_pos) {
-    const int key = min(tile * kTile + 16 * i, last_pos & ~15);
-    return (((int64_t)lane_of(p.page, base + i) * a.kv_heads + h) * a.B + (key & (a.B - 1))) * a.D;
+  static __device__ __forceinline__ void relative(Pages& p, float vref) {
+    const float v = fmaxf(p.vs - vref, -100.0f);
+    p.lv = v + kBias;
+    p.vi = exp2_(-v);
   }
+  static __device__ __forceinline__ int64_t at_of(const Pages& p, int i) {
+    return (int64_t)(uint32_t)lane_of((int)p.at, i) | (int64_t)lane_of((int)(p.at >> 32), i) << 32;
+  }
+  static __device__ __forceinline__ int dim(const Args& a) { return FULL ? DP : a.D; }
 
   // The bytes of this wave's 32 keys of a tile.
   struct Bytes {
     u32x4 k[2][DP / 64];
     Vec<uint32_t, VB / 4> v[8];
   };
-  static __device__ __forceinline__ Bytes load(const Args& a, const Pages& p, int base, int h, int tile, int last_pos) {
+  static __device__ __forceinline__ Bytes load(const Args& a, const Pages& p, int base) {
     const int lane = (int)threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), n = lane & 15,
               g = lane >> 4;
     Bytes b;
     // uniform addresses, and a lane's 32-bit offset from them; behind element D
     // - 1 the same key's first ones: q is zero there
-    const uint32_t vo = (uint32_t)(4 * g * a.D + (n * VB < a.D ? n * VB : 0));
+    const int D = dim(a);
+    const uint32_t vo = (uint32_t)(4 * g * D + (FULL || n * VB < D ? n * VB : 0));
 #pragma unroll
     for (int t = 0; t < 2; t++) {
-      const int64_t at = row_at(a, p, base, 2 * wave + t, h, tile, last_pos);
+      const int64_t at = at_of(p, base + 2 * wave + t);
 #pragma unroll
       for (int j = 0; j < DP / 64; j++)
-        b.k[t][j] = ld16(a.k + at + (uint32_t)(n * a.D + (j * 64 + g * 16 < a.D ? j * 64 + g * 16 : 0)));
+        b.k[t][j] = ld16(a.k + at + (uint32_t)(n * D + (FULL || j * 64 + g * 16 < D ? j * 64 + g * 16 : 0)));
 #pragma unroll
       for (int i = 0; i < 4; i++)
-        b.v[4 * t + i] = *reinterpret_cast<const Vec<uint32_t, VB / 4>*>(a.v + at + i * a.D + vo);
+        b.v[4 * t + i] = *reinterpret_cast<const Vec<uint32_t, VB / 4>*>(a.v + at + (uint32_t)(vo + i * D));
     }
     return b;
   }
@@ -131,7 +139,7 @@ struct Chunk {
     const int any_from = a.window > 0 ? max(task.first_pos - a.window + 1, 0) : 0;
 
     Pages pages = load_pages(a, table, h, begin, task.last_pos), next_pages = pages;
-    Bytes raw = load(a, pages, 0, h, begin, task.last_pos);
+    Bytes raw = load(a, pages, 0);
     for (int tile = begin; tile < end; tile++) {
       const int base = ((tile - begin) & 7) * kSubs;
       const int key0 = tile * kTile;
@@ -178,7 +186,7 @@ struct Chunk {
       }
       if (tile + 1 < end) {
         if (((tile + 1 - begin) & 7) == 0) next_pages = load_pages(a, table, h, tile + 1, task.last_pos);
-        raw = load(a, next_pages, ((tile + 1 - begin) & 7) * kSubs, h, tile + 1, task.last_pos);
+        raw = load(a, next_pages, ((tile + 1 - begin) & 7) * kSubs);
       }
       meet();  // the tile is there
       const bool nan_v = partial && *nan_word == tile;
@@ -187,6 +195,7 @@ struct Chunk {
       if (vmax > vref) {
         const float f = exp2_(vref - vmax);
         vref = vmax;
+        relative(pages, vref);
 #pragma unroll
         for (int r = 0; r < R; r++)
 #pragma unroll
@@ -219,10 +228,8 @@ struct Chunk {
 #pragma unroll
         for (int t = 0; t < 4; t++) {
           ks[t] = lane_of(pages.ks, sub0 + t);
-          const float v = lane_of(pages.vs, sub0 + t) - vref;
-          lv[t] = fmaxf(v, -100.0f);
-          vi[t] = exp2_(-lv[t]);
-          lv[t] += kBias;
+          lv[t] = lane_of(pages.lv, sub0 + t);
+          vi[t] = lane_of(pages.vi, sub0 + t);
         }
         if (partial) {
           const int from = seldom(half0);
@@ -242,10 +249,11 @@ struct Chunk {
         u32x4 pr[R][2];
 #pragma unroll
         for (int r = 0; r < R; r++) {
-          float mx = -kInf;
+          float mt[4];
 #pragma unroll
           for (int t = 0; t < 4; t++)
-            mx = fmaxf(mx, fmaxf(fmaxf(sc[r][t][0], sc[r][t][1]), fmaxf(sc[r][t][2], sc[r][t][3])) * ks[t]);
+            mt[t] = max3(max3(sc[r][t][0], sc[r][t][1], sc[r][t][2]), sc[r][t][3], sc[r][t][3]) * ks[t];
+          float mx = max3(max3(mt[0], mt[1], mt[2]), mt[3], mt[3]);
           if (__ballot(mx > m[r] + kSlack)) {
             mx = fmaxf(m[r], quad_max(mx));
             const float f = exp2_(m[r] - finite_or_0(mx));
@@ -294,7 +302,7 @@ struct Chunk {
             for (int i = 0; i < 8; i++) {
               const int sub = half * 4 + u * 2 + (i >> 2), key = key0 + 16 * sub + 4 * g + (i & 3);
               const uint32_t* v = reinterpret_cast<const uint32_t*>(
-                  a.v + row_at(a, pages, base, sub, h, tile, task.last_pos) + (4 * g + (i & 3)) * a.D + vd);
+                  a.v + at_of(pages, base + sub) + (4 * g + (i & 3)) * a.D + vd);
               const bool seen = key >= any_from && key <= task.last_pos;
 #pragma unroll
               for (int w = 0; w < VB / 4; w++) nan[w][i] = seen ? (((v[w] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7 : 0u;
@@ -326,7 +334,10 @@ struct Chunk {
           }
         }
       }
-      if (((tile + 1 - begin) & 7) == 0) pages = next_pages;
+      if (((tile + 1 - begin) & 7) == 0) {
+        pages = next_pages;
+        relative(pages, vref);
+      }
     }
 
     // ---- a lane holds elements 4g VB .. 4g VB + 4 VB - 1 of its row ----
@@ -364,13 +375,23 @@ struct Chunk {
 
 }  // namespace
 
+// The workspace does not depend on FULL.
 uint64_t attention_chunk_workspace_bytes(int64_t dim) {
-  return dim <= 64 ? workspace_bytes<Chunk<true, 64, 2>>() : workspace_bytes<Chunk<true, 128, 2>>();
+  return dim <= 64 ? workspace_bytes<Chunk<true, 64, 2, true>>() : workspace_bytes<Chunk<true, 128, 2, true>>();
 }
 
+namespace {
+template <bool BF16>
+hipError_t by_dim(Args& a, void* ws, uint64_t ws_bytes, hipStream_t s) {
+  if (a.D == 64) return go<Chunk<BF16, 64, 2, true>>(a, ws, ws_bytes, s);
+  if (a.D == 128) return go<Chunk<BF16, 128, 2, true>>(a, ws, ws_bytes, s);
+  if (a.D < 64) return go<Chunk<BF16, 64, 2, false>>(a, ws, ws_bytes, s);
+  return go<Chunk<BF16, 128, 2, false>>(a, ws, ws_bytes, s);
+}
+}  // namespace
+
 hipError_t launch_attention_chunk(bool bf16, Args& a, void* ws, uint64_t ws_bytes, hipStream_t s) {
-  if (a.D <= 64) return bf16 ? go<Chunk<true, 64, 2>>(a, ws, ws_bytes, s) : go<Chunk<false, 64, 2>>(a, ws, ws_bytes, s);
-  return bf16 ? go<Chunk<true, 128, 2>>(a, ws, ws_bytes, s) : go<Chunk<false, 128, 2>>(a, ws, ws_bytes, s);
+  return bf16 ? by_dim<true>(a, ws, ws_bytes, s) : by_dim<false>(a, ws, ws_bytes, s);
 }
 
 }  // namespace patch

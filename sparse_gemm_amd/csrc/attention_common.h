@@ -76,6 +76,13 @@ __device__ __forceinline__ int seldom(int x) {
   return x;
 }
 
+// Without the quieting of NaN operands that fmaxf's definition asks for.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+  return r;
+}
+
 // The largest of a row's four lanes (16 apart), and their sum.  A swap of two
 // copies' rows of 16 (halves of 32) leaves each lane both values.
 __device__ __forceinline__ void swapped(float x, float& a, float& b, bool by32) {
