@@ -55,6 +55,7 @@ using namespace attn;
 namespace {
 
 constexpr int kStep = 32;  // keys of a step
+constexpr int kWaves = 4, kThreads = 64 * kWaves;
 
 // The pages of a wave's next 64 steps, one step a lane; h: halves of a step
 // (16 keys lie in one page).  A page outside the cache reads page 0 with a
@@ -310,14 +311,15 @@ __device__ __forceinline__ void do_step(const Args& a, const Task& task, int ste
 template <bool BF16, int DP, int R>
 struct Few {
   static constexpr bool kBf16 = BF16;
-  static constexpr int kDim = DP, kRows = 16 * R, kStep = patch::kStep, kMinSteps = 8, kTaskCost = 8;
+  static constexpr int kWaves = patch::kWaves, kDim = DP, kRows = 16 * R, kStep = patch::kStep, kMinSteps = 8, kTaskCost = 8;
   static constexpr int kPerCu = R == 1 && DP <= 128 ? 2 : 1;
   static constexpr int kLds = kWaves * kRows * (DP + 4) + kWaves * kRows * 2 + kWaves;
 
   static __device__ __forceinline__ void run(const Args& a, const Seq& sq, const Task& task, int s, int h, int begin,
                                           int end, int part, float* lds) {
   constexpr int kLd = DP + 4, VB = DP / 16;
-  const int tid = (int)threadIdx.x, lane = tid & 63, wave = tid >> 6, n = lane & 15, g = lane >> 4;
+  const int tid = (int)threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), n = lane & 15,
+            g = lane >> 4;
   Rows<BF16, DP, R> x;
   const int32_t* table = a.table + s * a.table_row;
   int step = begin + wave;

@@ -26,13 +26,14 @@ constexpr int kSubs = kTile / 16;    // its sub-tiles of 16 keys, each in one pa
 __device__ __forceinline__ void meet() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
 // FULL: dim is DP, and a row's distance a constant.
-template <bool BF16, int DP, int R, bool FULL>
+template <bool BF16, int DP, int W, int R, bool FULL>
 struct Chunk {
   static constexpr bool kBf16 = BF16;
-  static constexpr int kDim = DP, kRows = kWaves * 16 * R, kStep = kTile, kMinSteps = 4, kTaskCost = 2;
+  static constexpr int kWaves = W, kDim = DP, kRows = W * 16 * R, kStep = kTile, kMinSteps = 4, kTaskCost = 2;
   static constexpr int kPerCu = 2;
   static constexpr int kFrags = DP / 16;                        // operands (1 KB) of 32 keys, of K as of V
-  static constexpr int kLds = kWaves * 2 * kFrags * 256 + 4;    // and a word that says that V held a NaN
+  static constexpr int kLds = kTile / 32 * 2 * kFrags * 256 + 4;  // and a word that says that V held a NaN
+  static constexpr int kOwn = kSubs / W;                        // sub-tiles that a wave brings in
   static constexpr int VB = DP / 16;                            // bytes of a V row in a lane
 
   // Pages of eight tiles, a sub-tile a lane.
@@ -68,10 +69,10 @@ struct Chunk {
   }
   static __device__ __forceinline__ int dim(const Args& a) { return FULL ? DP : a.D; }
 
-  // The bytes of this wave's 32 keys of a tile.
+  // The bytes of this wave's sub-tiles of a tile.
   struct Bytes {
-    u32x4 k[2][DP / 64];
-    Vec<uint32_t, VB / 4> v[8];
+    u32x4 k[kOwn][DP / 64];
+    Vec<uint32_t, VB / 4> v[kOwn][4];
   };
   static __device__ __forceinline__ Bytes load(const Args& a, const Pages& p, int base) {
     const int lane = (int)threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), n = lane & 15,
@@ -82,23 +83,23 @@ struct Chunk {
     const int D = dim(a);
     const uint32_t vo = (uint32_t)(4 * g * D + (FULL || n * VB < D ? n * VB : 0));
 #pragma unroll
-    for (int t = 0; t < 2; t++) {
-      const int64_t at = at_of(p, base + 2 * wave + t);
+    for (int t = 0; t < kOwn; t++) {
+      const int64_t at = at_of(p, base + wave * kOwn + t);
 #pragma unroll
       for (int j = 0; j < DP / 64; j++)
         b.k[t][j] = ld16(a.k + at + (uint32_t)(n * D + (FULL || j * 64 + g * 16 < D ? j * 64 + g * 16 : 0)));
 #pragma unroll
       for (int i = 0; i < 4; i++)
-        b.v[4 * t + i] = *reinterpret_cast<const Vec<uint32_t, VB / 4>*>(a.v + at + (uint32_t)(vo + i * D));
+        b.v[t][i] = *reinterpret_cast<const Vec<uint32_t, VB / 4>*>(a.v + at + (uint32_t)(vo + i * D));
     }
     return b;
   }
 
   static __device__ __forceinline__ void run(const Args& a, const Seq& sq, const Task& task, int s, int h, int begin,
                                              int end, int part, float* lds) {
-    const int tid = (int)threadIdx.x, lane = tid & 63, wave = tid >> 6, n = lane & 15, g = lane >> 4;
+    const int tid = (int)threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), n = lane & 15, g = lane >> 4;
     u32x4* const frags = reinterpret_cast<u32x4*>(lds);  // [32 keys][K, V][operand][lane]
-    int* const nan_word = reinterpret_cast<int*>(lds + kWaves * 2 * kFrags * 256);
+    int* const nan_word = reinterpret_cast<int*>(lds + kTile / 32 * 2 * kFrags * 256);
     const int32_t* table = a.table + s * a.table_row;
     const int row0 = task.r0 + wave * 16 * R;
 
@@ -145,43 +146,50 @@ struct Chunk {
       const int key0 = tile * kTile;
       const bool partial = key0 < all_from || key0 + kTile - 1 > task.first_pos;
       meet();  // the last tile has been read
-      // ---- this wave's 32 keys into LDS ----
-      {
-        u32x4* kf = frags + (wave * 2) * kFrags * 64 + lane;
-        u32x4* vf = kf + kFrags * 64;
-        if (partial) {
-          const int from = seldom(key0);
-          bool has = false;
+      // ---- this wave's sub-tiles into LDS: operands of K, halves of operands of V ----
+      if (partial) {
+        const int from = seldom(key0);
+        bool has = false;
 #pragma unroll
-          for (int i = 0; i < 8; i++) {
-            const int key = from + wave * 32 + (i >> 2) * 16 + 4 * g + (i & 3);
+        for (int t = 0; t < kOwn; t++)
+#pragma unroll
+          for (int i = 0; i < 4; i++) {
+            const int key = from + (wave * kOwn + t) * 16 + 4 * g + i;
             const bool seen = key >= any_from && key <= task.last_pos;
 #pragma unroll
             for (int w = 0; w < VB / 4; w++) {
-              const uint32_t v = seen ? raw.v[i].v[w] : 0u;
+              const uint32_t v = seen ? raw.v[t][i].v[w] : 0u;
               const uint32_t hit = ((v & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
               has |= hit != 0;
-              raw.v[i].v[w] = v & ~((hit >> 7) * 0xffu);
+              raw.v[t][i].v[w] = v & ~((hit >> 7) * 0xffu);
             }
           }
-          if (__ballot(has) && lane == 0) *nan_word = tile;
+        if (__ballot(has) && lane == 0) *nan_word = tile;
+      }
+#pragma unroll
+      for (int t = 0; t < kOwn; t++) {
+        const int sub = wave * kOwn + t;
+        u32x4* kf = frags + ((sub >> 1) * 2 * kFrags + (sub & 1) * (DP / 32)) * 64 + lane;
+#pragma unroll
+        for (int j = 0; j < DP / 64; j++) {
+          kf[(2 * j) * 64] = widen8<BF16>(raw.k[t][j][0], raw.k[t][j][1]);
+          kf[(2 * j + 1) * 64] = widen8<BF16>(raw.k[t][j][2], raw.k[t][j][3]);
         }
-#pragma unroll
-        for (int t = 0; t < 2; t++)
-#pragma unroll
-          for (int j = 0; j < DP / 64; j++) {
-            kf[(t * (DP / 32) + 2 * j) * 64] = widen8<BF16>(raw.k[t][j][0], raw.k[t][j][1]);
-            kf[(t * (DP / 32) + 2 * j + 1) * 64] = widen8<BF16>(raw.k[t][j][2], raw.k[t][j][3]);
-          }
+        u32x2* vf = reinterpret_cast<u32x2*>(frags + ((sub >> 1) * 2 + 1) * kFrags * 64 + lane) + (sub & 1);
 #pragma unroll
         for (int w = 0; w < VB / 4; w++) {
-          uint32_t v[8];
+          u32x2 e[4];
 #pragma unroll
-          for (int i = 0; i < 8; i++) v[i] = raw.v[i].v[w];
-          u32x4 e[4];
-          zip4(v, e);
+          for (int p = 0; p < 2; p++) {
+            uint32_t w0, w1, w2, w3;
+            zip2(raw.v[t][2 * p].v[w], raw.v[t][2 * p + 1].v[w], w0, w1, w2, w3);
+            e[0][p] = w0;
+            e[1][p] = w1;
+            e[2][p] = w2;
+            e[3][p] = w3;
+          }
 #pragma unroll
-          for (int j = 0; j < 4; j++) vf[(4 * w + j) * 64] = e[j];
+          for (int j = 0; j < 4; j++) vf[(4 * w + j) * 128] = e[j];
         }
       }
       if (tile + 1 < end) {
@@ -346,7 +354,7 @@ struct Chunk {
 #pragma unroll
     for (int r = 0; r < R; r++) {
       l[r] = quad_sum(l[r]);
-      const int row = wave * 16 * R + r * 16 + n;  // of the task
+      const int row = (wave * R + r) * 16 + n;  // of the task
       if (task.r0 + row >= task.r1) continue;
       const float by = l[r] == 0.f || vref <= kNoScale ? 0.f : exp2_(vref) / l[r];
       if (a.lse && g == 0 && part < 0) store_lse(a, sq, h, task.r0 + row, lse_of(m[r], l[r]));
@@ -377,16 +385,16 @@ struct Chunk {
 
 // The workspace does not depend on FULL.
 uint64_t attention_chunk_workspace_bytes(int64_t dim) {
-  return dim <= 64 ? workspace_bytes<Chunk<true, 64, 2, true>>() : workspace_bytes<Chunk<true, 128, 2, true>>();
+  return dim <= 64 ? workspace_bytes<Chunk<true, 64, 4, 2, true>>() : workspace_bytes<Chunk<true, 128, 4, 2, true>>();
 }
 
 namespace {
 template <bool BF16>
 hipError_t by_dim(Args& a, void* ws, uint64_t ws_bytes, hipStream_t s) {
-  if (a.D == 64) return go<Chunk<BF16, 64, 2, true>>(a, ws, ws_bytes, s);
-  if (a.D == 128) return go<Chunk<BF16, 128, 2, true>>(a, ws, ws_bytes, s);
-  if (a.D < 64) return go<Chunk<BF16, 64, 2, false>>(a, ws, ws_bytes, s);
-  return go<Chunk<BF16, 128, 2, false>>(a, ws, ws_bytes, s);
+  if (a.D == 64) return go<Chunk<BF16, 64, 4, 2, true>>(a, ws, ws_bytes, s);
+  if (a.D == 128) return go<Chunk<BF16, 128, 4, 2, true>>(a, ws, ws_bytes, s);
+  if (a.D < 64) return go<Chunk<BF16, 64, 4, 2, false>>(a, ws, ws_bytes, s);
+  return go<Chunk<BF16, 128, 4, 2, false>>(a, ws, ws_bytes, s);
 }
 }  // namespace
 

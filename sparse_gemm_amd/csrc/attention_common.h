@@ -3,7 +3,7 @@
 //
 // A kernel's body says how a workgroup attends to a range of keys for the
 // rows of one task:
-//   kBf16, kDim (elements of a head, padded), kRows (of a task), kStep (keys of
+//   kBf16, kWaves (of a workgroup), kDim (elements of a head, padded), kRows (of a task), kStep (keys of
 //   a step), kMinSteps (of a workgroup, at least), kTaskCost (what a task costs
 //   beside its steps, in steps), kPerCu (workgroups a CU), kLds (its LDS, floats),
 //   run(a, sq, task, s, h, begin, end, part, lds): the steps begin .. end - 1;
@@ -21,8 +21,6 @@
 namespace patch {
 namespace attn {
 
-constexpr int kWaves = 4;
-constexpr int kThreads = 64 * kWaves;
 // Probabilities are 2^(s - m + kBias), m being within kSlack of the running
 // maximum: sums and outputs are only scaled anew when it grows by more.  2^14
 // at most, and 2^-20 of the maximum still in fp16's normal range.
@@ -30,6 +28,9 @@ constexpr float kBias = 6.0f, kSlack = 8.0f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kInf = __builtin_inff();
+
+template <class Body>
+constexpr int threads_of = 64 * Body::kWaves;
 
 struct Args {
   const uint16_t* q;
@@ -72,7 +73,7 @@ __device__ __forceinline__ u32x4 widen8(uint32_t lo, uint32_t hi) {
 // A value for use in a block that seldom runs: what is computed from it stays
 // in the block (the compiler would rather compute it every time and select).
 __device__ __forceinline__ int seldom(int x) {
-  asm volatile("" : "+s"(x));
+  asm volatile("" : "+v"(x));
   return x;
 }
 
@@ -105,17 +106,25 @@ __device__ __forceinline__ float quad_sum(float x) {
   return a + b;
 }
 
-// Four neighbouring elements of 8 keys (a word a key) as four A operands of
-// V^T, a byte of each key.
+// Four neighbouring elements of two keys (a word each) as pairs: a word of
+// each element's two.
+__device__ __forceinline__ void zip2(uint32_t k0, uint32_t k1, uint32_t& e0, uint32_t& e1, uint32_t& e2, uint32_t& e3) {
+  const uint32_t z0 = __builtin_amdgcn_perm(k1, k0, 0x05010400u), z1 = __builtin_amdgcn_perm(k1, k0, 0x07030602u);
+  e0 = widen2<false, false>(z0);
+  e1 = widen2<false, true>(z0);
+  e2 = widen2<false, false>(z1);
+  e3 = widen2<false, true>(z1);
+}
+// Four neighbouring elements of 8 keys as four A operands of V^T.
 __device__ __forceinline__ void zip4(const uint32_t (&v)[8], u32x4 (&e)[4]) {
 #pragma unroll
   for (int p = 0; p < 4; p++) {
-    const uint32_t z0 = __builtin_amdgcn_perm(v[2 * p + 1], v[2 * p], 0x05010400u);
-    const uint32_t z1 = __builtin_amdgcn_perm(v[2 * p + 1], v[2 * p], 0x07030602u);
-    e[0][p] = widen2<false, false>(z0);
-    e[1][p] = widen2<false, true>(z0);
-    e[2][p] = widen2<false, false>(z1);
-    e[3][p] = widen2<false, true>(z1);
+    uint32_t w0, w1, w2, w3;
+    zip2(v[2 * p], v[2 * p + 1], w0, w1, w2, w3);
+    e[0][p] = w0;
+    e[1][p] = w1;
+    e[2][p] = w2;
+    e[3][p] = w3;
   }
 }
 
@@ -209,13 +218,13 @@ __device__ __forceinline__ void store_lse(const Args& a, const Seq& sq, int h, i
 }
 __device__ __forceinline__ float lse_of(float m, float l) { return (m + __log2f(l) - kBias) * kLn2; }
 
-template <bool BF16>
+template <class Body>
 __device__ __forceinline__ void fill_rows(const Args& a, const Seq& sq, const Task& t, int h) {
   const float o = sq.bad ? __builtin_nanf("") : 0.f, lse = sq.bad ? __builtin_nanf("") : -kInf;
   const int chunks = a.D / 8;
-  for (int e = threadIdx.x; e < (t.r1 - t.r0) * chunks; e += kThreads) {
+  for (int e = threadIdx.x; e < (t.r1 - t.r0) * chunks; e += threads_of<Body>) {
     const int row = t.r0 + e / chunks, d = e % chunks * 8;
-    store8<BF16>(a, out_at(a, sq, h, row, d), {o, o, o, o, o, o, o, o});
+    store8<Body::kBf16>(a, out_at(a, sq, h, row, d), {o, o, o, o, o, o, o, o});
     if (a.lse && d == 0) store_lse(a, sq, h, row, lse);
   }
 }
@@ -230,7 +239,7 @@ template <class Body>
 __device__ __forceinline__ void join_parts(const Args& a, const Seq& sq, const Task& task, int h, int w0, int count) {
   constexpr int kRows = Body::kRows, DP = Body::kDim, kSlot = kRows * (DP + 2);
   const int chunks = a.D / 8;
-  for (int e = threadIdx.x; e < (task.r1 - task.r0) * chunks; e += kThreads) {
+  for (int e = threadIdx.x; e < (task.r1 - task.r0) * chunks; e += threads_of<Body>) {
     const int row = e / chunks, d = (e - row * chunks) * 8;
     float mx = -kInf, sum = 0.f, acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
@@ -286,13 +295,14 @@ struct LaneLine {
 };
 
 // For more sequences: a prefix sum in LDS, by the whole workgroup.
+template <class Body>
 struct LdsLine {
   int* line;  // [S + 1]: where sequence s begins
   int total, S;
   template <typename F>
   __device__ __forceinline__ LdsLine(int n_seqs, int* l, int* wave_sum, F cost) : line(l), total(0), S(n_seqs) {
     const int tid = (int)threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int each = (S + kThreads - 1) / kThreads, s1 = min((tid + 1) * each, S);
+    const int each = (S + threads_of<Body> - 1) / threads_of<Body>, s1 = min((tid + 1) * each, S);
     int mine = 0;
     for (int s = tid * each; s < s1; s++) {
       line[s] = cost(s);
@@ -307,7 +317,7 @@ struct LdsLine {
     if (lane == 63) wave_sum[wave] = upto;
     __syncthreads();
     int at = upto - mine;
-    for (int w = 0; w < kWaves; w++) {
+    for (int w = 0; w < Body::kWaves; w++) {
       if (w < wave) at += wave_sum[w];
       total += wave_sum[w];
     }
@@ -333,7 +343,7 @@ template <class Body>
 __device__ __forceinline__ void run_piece(const Args& a, const Seq& sq, const Task& task, int s, int h, int begin,
                                           int end, int w0, int count, float* lds, int* joined) {
   if (task.fill) {
-    fill_rows<Body::kBf16>(a, sq, task, h);
+    fill_rows<Body>(a, sq, task, h);
     return;
   }
   const int lane = (int)threadIdx.x & 63;
@@ -371,9 +381,9 @@ __device__ __forceinline__ void run_piece(const Args& a, const Seq& sq, const Ta
 // on which a task begins with Body::kTaskCost places that stand for what it costs
 // beside its steps: about what that many steps take.
 template <class Body, bool MANY>
-__global__ __launch_bounds__(kThreads, Body::kPerCu) void k_attention_line(Args a) {
+__global__ __launch_bounds__(threads_of<Body>, Body::kPerCu* Body::kWaves / 4) void k_attention_line(Args a) {
   extern __shared__ __align__(16) float lds[];
-  __shared__ int wave_sum[kWaves];
+  __shared__ int wave_sum[Body::kWaves];
   __shared__ int joined;
   constexpr int kTaskCost = Body::kTaskCost;
   const int lane = (int)threadIdx.x & 63;
@@ -385,7 +395,7 @@ __global__ __launch_bounds__(kThreads, Body::kPerCu) void k_attention_line(Args 
   };
   const auto make = [&](auto f) {  // a line of f(sequence) for every head
     if constexpr (MANY)
-      return LdsLine(a.S, reinterpret_cast<int*>(lds + Body::kLds), wave_sum,
+      return LdsLine<Body>(a.S, reinterpret_cast<int*>(lds + Body::kLds), wave_sum,
                      [&](int s) { return f(seq_of(a, s)) * a.kv_heads; });
     else
       return LaneLine(lane < a.S ? f(mine) * a.kv_heads : 0);
@@ -436,7 +446,7 @@ __global__ __launch_bounds__(kThreads, Body::kPerCu) void k_attention_line(Args 
 // floor(cu[s] group / rows) + s up to the same of s + 1 for each head, at
 // least as many as its rows need.
 template <class Body>
-__global__ __launch_bounds__(kThreads, Body::kPerCu) void k_attention_task(Args a) {
+__global__ __launch_bounds__(threads_of<Body>, Body::kPerCu* Body::kWaves / 4) void k_attention_task(Args a) {
   extern __shared__ __align__(16) float lds[];
   constexpr int kRows = Body::kRows;
   const int h = (int)(blockIdx.x % (uint32_t)a.kv_heads);
@@ -447,20 +457,20 @@ __global__ __launch_bounds__(kThreads, Body::kPerCu) void k_attention_task(Args 
   if (slot < first || (slot - first) * kRows >= (int64_t)sq.n * a.group) return;
   const Task task = task_of<Body>(a, sq, (int)(slot - first));
   if (task.fill)
-    fill_rows<Body::kBf16>(a, sq, task, h);
+    fill_rows<Body>(a, sq, task, h);
   else
     Body::run(a, sq, task, s, h, task.begin, task.end, -1, lds);
 }
 
 // ---- launch ----
-inline hipError_t launch(const void* fn, int64_t blocks, size_t lds, Args& a, hipStream_t s) {
+inline hipError_t launch(const void* fn, int threads, int64_t blocks, size_t lds, Args& a, hipStream_t s) {
   if (blocks > 0x7fffffff) return hipErrorInvalidValue;
   if (lds > 65536) {
     hipError_t e = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
     if (e != hipSuccess) return e;
   }
   void* args[] = {&a};
-  return hipLaunchKernel(fn, dim3((unsigned)blocks), dim3(kThreads), args, lds, s);
+  return hipLaunchKernel(fn, dim3((unsigned)blocks), dim3((unsigned)threads), args, lds, s);
 }
 
 template <class Body>
@@ -486,10 +496,10 @@ hipError_t go(Args& a, void* ws, uint64_t ws_bytes, hipStream_t s) {
     a.flags = reinterpret_cast<uint64_t*>(ws);
     a.parts = reinterpret_cast<float*>(a.flags + 2 * n);
     a.token = launch_token();
-    return a.S > 64 ? launch(reinterpret_cast<const void*>(k_attention_line<Body, true>), n, lds + 4 * (size_t)(a.S + 1), a, s)
-                    : launch(reinterpret_cast<const void*>(k_attention_line<Body, false>), n, lds, a, s);
+    return a.S > 64 ? launch(reinterpret_cast<const void*>(k_attention_line<Body, true>), threads_of<Body>, n, lds + 4 * (size_t)(a.S + 1), a, s)
+                    : launch(reinterpret_cast<const void*>(k_attention_line<Body, false>), threads_of<Body>, n, lds, a, s);
   }
-  return launch(reinterpret_cast<const void*>(k_attention_task<Body>), tasks, lds, a, s);
+  return launch(reinterpret_cast<const void*>(k_attention_task<Body>), threads_of<Body>, tasks, lds, a, s);
 }
 
 }  // namespace attn
