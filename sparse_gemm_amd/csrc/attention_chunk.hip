@@ -11,7 +11,7 @@
 // joined at the end; two workgroups a CU fill each other's waits.
 //
 // The products, the running maximum and sum, and the order of the keys inside
-// an operand are those of attention.hip; 64 keys are treated at once.
+// an operand are those of attention.hip.
 #include "attention_common.h"
 
 namespace patch {
@@ -93,6 +93,23 @@ struct Chunk {
         b.v[t][i] = *reinterpret_cast<const Vec<uint32_t, VB / 4>*>(a.v + at + (uint32_t)(vo + i * D));
     }
     return b;
+  }
+
+  // Scores of 32 keys, whose operands begin at `at`, for the wave's rows.
+  template <int RR>
+  static __device__ __forceinline__ void scores(const u32x4* at, const u32x4 (&q)[RR][DP / 32], f32x4 (&sc)[RR][2]) {
+#pragma unroll
+    for (int t = 0; t < 2; t++)
+#pragma unroll
+      for (int r = 0; r < RR; r++) sc[r][t] = (f32x4){0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < DP / 32; j++)
+#pragma unroll
+      for (int t = 0; t < 2; t++) {
+        const u32x4 k = at[(t * (DP / 32) + j) * 64];
+#pragma unroll
+        for (int r = 0; r < RR; r++) sc[r][t] = mma_dense<BF16>(k, q[r][j], sc[r][t]);
+      }
   }
 
   static __device__ __forceinline__ void run(const Args& a, const Seq& sq, const Task& task, int s, int h, int begin,
@@ -210,135 +227,128 @@ struct Chunk {
           for (int j = 0; j < DP / 16; j++) o[r][j] *= f;
       }
 
-      for (int half = 0; half < 2; half++) {  // 64 keys
-        const int sub0 = base + half * 4, half0 = key0 + half * 64;
-        if (half0 > task.last_pos) break;
-        f32x4 sc[R][4];
+      // 32 keys at a time; the next ones' scores are computed between this
+      // one's exponentials
+      f32x4 sc[2][R][2];
+      scores<R>(frags + lane, q, sc[0]);
 #pragma unroll
-        for (int t = 0; t < 4; t++)
+      for (int st = 0; st < kTile / 32; st++) {
+        f32x4(&cur)[R][2] = sc[st & 1];
+        const int sub0 = base + st * 2, from0 = key0 + st * 32;
+        float ks[2], lv[2], vi[2];
 #pragma unroll
-          for (int r = 0; r < R; r++) sc[r][t] = (f32x4){0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int j = 0; j < DP / 32; j++) {
-          u32x4 k[4];
-#pragma unroll
-          for (int t = 0; t < 4; t++)
-            k[t] = frags[((half * 2 + (t >> 1)) * 2) * kFrags * 64 + ((t & 1) * (DP / 32) + j) * 64 + lane];
-#pragma unroll
-          for (int t = 0; t < 4; t++)
-#pragma unroll
-            for (int r = 0; r < R; r++) sc[r][t] = mma_dense<BF16>(k[t], q[r][j], sc[r][t]);
-        }
-        // probabilities times the v scale (relative to vref): 2^(s + log2(vs) - m
-        // + kBias), one multiply-add and the exponential; the sum takes them
-        // divided by it again
-        float ks[4], lv[4], vi[4];
-#pragma unroll
-        for (int t = 0; t < 4; t++) {
+        for (int t = 0; t < 2; t++) {
           ks[t] = lane_of(pages.ks, sub0 + t);
           lv[t] = lane_of(pages.lv, sub0 + t);
           vi[t] = lane_of(pages.vi, sub0 + t);
         }
         if (partial) {
-          const int from = seldom(half0);
+          const int from = seldom(from0);
 #pragma unroll
-          for (int t = 0; t < 4; t++) {
+          for (int t = 0; t < 2; t++) {
 #pragma unroll
             for (int r = 0; r < R; r++)
 #pragma unroll
               for (int i = 0; i < 4; i++) {
                 const int key = from + 16 * t + 4 * g + i;
                 const bool seen = key <= hi[r] && key >= lo[r] && key <= task.last_pos;
-                sc[r][t][i] = seen ? sc[r][t][i] * ks[t] : -kInf;
+                cur[r][t][i] = seen ? cur[r][t][i] * ks[t] : -kInf;
               }
             ks[t] = 1.0f;
           }
         }
-        u32x4 pr[R][2];
+        float mx[R];
+        bool grows = false;
 #pragma unroll
         for (int r = 0; r < R; r++) {
-          float mt[4];
+          float mt[2];
 #pragma unroll
-          for (int t = 0; t < 4; t++)
-            mt[t] = max3(max3(sc[r][t][0], sc[r][t][1], sc[r][t][2]), sc[r][t][3], sc[r][t][3]) * ks[t];
-          float mx = max3(max3(mt[0], mt[1], mt[2]), mt[3], mt[3]);
-          if (__ballot(mx > m[r] + kSlack)) {
-            mx = fmaxf(m[r], quad_max(mx));
-            const float f = exp2_(m[r] - finite_or_0(mx));
-            m[r] = mx;
+          for (int t = 0; t < 2; t++)
+            mt[t] = max3(max3(cur[r][t][0], cur[r][t][1], cur[r][t][2]), cur[r][t][3], cur[r][t][3]) * ks[t];
+          mx[r] = max3(mt[0], mt[1], mt[1]);
+          grows |= mx[r] > m[r] + kSlack;
+        }
+        if (__ballot(grows)) {
+#pragma unroll
+          for (int r = 0; r < R; r++) {
+            const float mn = fmaxf(m[r], quad_max(mx[r]));
+            const float f = exp2_(m[r] - finite_or_0(mn));
+            m[r] = mn;
             l[r] *= f;
 #pragma unroll
             for (int j = 0; j < DP / 16; j++) o[r][j] *= f;
           }
+        }
+        if (st + 1 < kTile / 32) scores<R>(frags + (st + 1) * 2 * kFrags * 64 + lane, q, sc[(st + 1) & 1]);
+        // probabilities times the v scale (relative to vref): 2^(s + log2(vs) - m
+        // + kBias), one multiply-add and the exponential; the sum takes them
+        // divided by it again
+        u32x4 pr[R];
+#pragma unroll
+        for (int r = 0; r < R; r++) {
           const float mu = finite_or_0(m[r]);
+          f16x8 ph;
 #pragma unroll
-          for (int u = 0; u < 2; u++) {
-            f16x8 ph;
+          for (int t = 0; t < 2; t++) {
+            const float off = lv[t] - mu;
+            float sum = 0.f;
 #pragma unroll
-            for (int t = 0; t < 2; t++) {
-              const float off = lv[2 * u + t] - mu;
-              float sum = 0.f;
-#pragma unroll
-              for (int i = 0; i < 4; i++) {
-                const float e = exp2_(fmaf(sc[r][2 * u + t][i], ks[2 * u + t], off));
-                sum += e;
-                ph[4 * t + i] = (_Float16)e;
-              }
-              l[r] = fmaf(sum, vi[2 * u + t], l[r]);
+            for (int i = 0; i < 4; i++) {
+              const float e = exp2_(fmaf(cur[r][t][i], ks[t], off));
+              sum += e;
+              ph[4 * t + i] = (_Float16)e;
             }
-            pr[r][u] = __builtin_bit_cast(u32x4, ph);
+            l[r] = fmaf(sum, vi[t], l[r]);
           }
+          pr[r] = __builtin_bit_cast(u32x4, ph);
         }
+        const u32x4* vf = frags + (st * 2 + 1) * kFrags * 64 + lane;
 #pragma unroll
-        for (int u = 0; u < 2; u++) {
-          const u32x4* vf = frags + ((half * 2 + u) * 2 + 1) * kFrags * 64 + lane;
+        for (int j = 0; j < DP / 16; j++) {
+          const u32x4 v = vf[j * 64];
 #pragma unroll
-          for (int j = 0; j < DP / 16; j++) {
-            const u32x4 v = vf[j * 64];
-#pragma unroll
-            for (int r = 0; r < R; r++) o[r][j] = mma_dense<false>(v, pr[r][u], o[r][j]);
-          }
+          for (int r = 0; r < R; r++) o[r][j] = mma_dense<false>(v, pr[r], o[r][j]);
         }
-        if (nan_v) {
-          // rare: V holds NaN in a row that not every row of the task sees (as in attention.hip)
-          const int vd = n * VB < a.D ? n * VB : 0;
+      }
+      if (nan_v) {
+        // rare: V holds NaN in a row that not every row of the task sees (as in attention.hip)
+        const int vd = n * VB < a.D ? n * VB : 0;
 #pragma unroll 1
-          for (int u = 0; u < 2; u++) {
-            u32x4 see[R];
-            uint32_t nan[VB / 4][8];
+        for (int st = 0; st < kTile / 32; st++) {
+          u32x4 see[R];
+          const int from0 = seldom(key0 + st * 32);
+#pragma unroll
+          for (int r = 0; r < R; r++) {
+            f16x8 one;
 #pragma unroll
             for (int i = 0; i < 8; i++) {
-              const int sub = half * 4 + u * 2 + (i >> 2), key = key0 + 16 * sub + 4 * g + (i & 3);
-              const uint32_t* v = reinterpret_cast<const uint32_t*>(
-                  a.v + at_of(pages, base + sub) + (4 * g + (i & 3)) * a.D + vd);
-              const bool seen = key >= any_from && key <= task.last_pos;
-#pragma unroll
-              for (int w = 0; w < VB / 4; w++) nan[w][i] = seen ? (((v[w] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7 : 0u;
+              const int key = from0 + (i >> 2) * 16 + 4 * g + (i & 3);
+              one[i] = key <= hi[r] && key >= lo[r] && key <= task.last_pos ? (_Float16)1.0f : (_Float16)0.0f;
             }
+            see[r] = __builtin_bit_cast(u32x4, one);
+          }
 #pragma unroll
-            for (int r = 0; r < R; r++) {
-              f16x8 one;
+          for (int w = 0; w < VB / 4; w++) {
+            uint32_t nan[8];
 #pragma unroll
-              for (int i = 0; i < 8; i++) {
-                const int key = half0 + u * 32 + (i >> 2) * 16 + 4 * g + (i & 3);
-                one[i] = key <= hi[r] && key >= lo[r] && key <= task.last_pos ? (_Float16)1.0f : (_Float16)0.0f;
+            for (int i = 0; i < 8; i++) {
+              const int key = from0 + (i >> 2) * 16 + 4 * g + (i & 3);
+              const uint32_t v = *reinterpret_cast<const uint32_t*>(
+                  a.v + at_of(pages, base + st * 2 + (i >> 2)) + (4 * g + (i & 3)) * a.D + vd + 4 * w);
+              nan[i] =
+                  key >= any_from && key <= task.last_pos ? (((v & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7 : 0u;
+            }
+            u32x4 e[4];
+            zip4(nan, e);
+#pragma unroll
+            for (int j = 0; j < 4; j++)
+#pragma unroll
+              for (int r = 0; r < R; r++) {
+                const f32x4 hit = mma_dense<false>(e[j], see[r], (f32x4){0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+                for (int i = 0; i < 4; i++)
+                  if (hit[i] > 0.f) o[r][4 * w + j][i] = __builtin_nanf("");
               }
-              see[r] = __builtin_bit_cast(u32x4, one);
-            }
-#pragma unroll
-            for (int w = 0; w < VB / 4; w++) {
-              u32x4 e[4];
-              zip4(nan[w], e);
-#pragma unroll
-              for (int j = 0; j < 4; j++)
-#pragma unroll
-                for (int r = 0; r < R; r++) {
-                  const f32x4 hit = mma_dense<false>(e[j], see[r], (f32x4){0.f, 0.f, 0.f, 0.f});
-#pragma unroll
-                  for (int i = 0; i < 4; i++)
-                    if (hit[i] > 0.f) o[r][4 * w + j][i] = __builtin_nanf("");
-                }
-            }
           }
         }
       }
