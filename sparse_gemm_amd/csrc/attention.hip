@@ -436,7 +436,7 @@ uint64_t launch_token() {
 }  // namespace attn
 
 uint64_t attention_workspace_bytes(int64_t T, int64_t S, int64_t heads, int64_t kv_heads, int64_t dim) {
-  if (many_rows(T, S, heads / kv_heads, dim)) return attention_chunk_workspace_bytes(dim);
+  if (many_rows(T, S, heads / kv_heads, dim)) return attention_chunk_workspace_bytes(T, S, heads / kv_heads, dim);
   const int R = tile_rows(T, S, heads / kv_heads, dim);
   if (dim <= 64) return R == 1 ? workspace_bytes<Few<true, 64, 1>>() : workspace_bytes<Few<true, 64, 2>>();
   if (dim <= 128) return R == 1 ? workspace_bytes<Few<true, 128, 1>>() : workspace_bytes<Few<true, 128, 2>>();

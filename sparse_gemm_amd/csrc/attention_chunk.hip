@@ -26,14 +26,14 @@ constexpr int kSubs = kTile / 16;    // its sub-tiles of 16 keys, each in one pa
 __device__ __forceinline__ void meet() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
 // FULL: dim is DP, and a row's distance a constant.
-template <bool BF16, int DP, int W, int R, bool FULL>
+template <bool BF16, int DP, int R, bool FULL>
 struct Chunk {
   static constexpr bool kBf16 = BF16;
-  static constexpr int kWaves = W, kDim = DP, kRows = W * 16 * R, kStep = kTile, kMinSteps = 4, kTaskCost = 2;
-  static constexpr int kPerCu = 2;
+  static constexpr int kWaves = 8, kDim = DP, kRows = kWaves * 16 * R, kStep = kTile, kMinSteps = 4, kTaskCost = 2;
+  static constexpr int kPerCu = 1;
   static constexpr int kFrags = DP / 16;                        // operands (1 KB) of 32 keys, of K as of V
-  static constexpr int kLds = kTile / 32 * 2 * kFrags * 256 + 4;  // and a word that says that V held a NaN
-  static constexpr int kOwn = kSubs / W;                        // sub-tiles that a wave brings in
+  static constexpr int kBuf = kTile / 32 * 2 * kFrags * 64;       // 16-byte words of a tile
+  static constexpr int kLds = 2 * (kBuf * 4 + 1) + 2;             // two, each with a word that says that V held a NaN
   static constexpr int VB = DP / 16;                            // bytes of a V row in a lane
 
   // Pages of eight tiles, a sub-tile a lane.
@@ -69,30 +69,72 @@ struct Chunk {
   }
   static __device__ __forceinline__ int dim(const Args& a) { return FULL ? DP : a.D; }
 
-  // The bytes of this wave's sub-tiles of a tile.
+  // The bytes of this wave's sub-tile of a tile.
   struct Bytes {
-    u32x4 k[kOwn][DP / 64];
-    Vec<uint32_t, VB / 4> v[kOwn][4];
+    u32x4 k[DP / 64];
+    Vec<uint32_t, VB / 4> v[4];
   };
-  static __device__ __forceinline__ Bytes load(const Args& a, const Pages& p, int base) {
-    const int lane = (int)threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), n = lane & 15,
-              g = lane >> 4;
+  static __device__ __forceinline__ Bytes load(const Args& a, int64_t at) {
+    const int lane = (int)threadIdx.x & 63, n = lane & 15, g = lane >> 4;
     Bytes b;
     // uniform addresses, and a lane's 32-bit offset from them; behind element D
     // - 1 the same key's first ones: q is zero there
     const int D = dim(a);
     const uint32_t vo = (uint32_t)(4 * g * D + (FULL || n * VB < D ? n * VB : 0));
 #pragma unroll
-    for (int t = 0; t < kOwn; t++) {
-      const int64_t at = at_of(p, base + wave * kOwn + t);
+    for (int j = 0; j < DP / 64; j++)
+      b.k[j] = ld16(a.k + at + (uint32_t)(n * D + (FULL || j * 64 + g * 16 < D ? j * 64 + g * 16 : 0)));
 #pragma unroll
-      for (int j = 0; j < DP / 64; j++)
-        b.k[t][j] = ld16(a.k + at + (uint32_t)(n * D + (FULL || j * 64 + g * 16 < D ? j * 64 + g * 16 : 0)));
-#pragma unroll
-      for (int i = 0; i < 4; i++)
-        b.v[t][i] = *reinterpret_cast<const Vec<uint32_t, VB / 4>*>(a.v + at + (uint32_t)(vo + i * D));
-    }
+    for (int i = 0; i < 4; i++)
+      b.v[i] = *reinterpret_cast<const Vec<uint32_t, VB / 4>*>(a.v + at + (uint32_t)(vo + i * D));
     return b;
+  }
+  // Into LDS: operands of K, and halves of operands of V.  `mask`: V rows that
+  // no row of the task sees hold anything at all: take zeros.  A NaN in a row
+  // that some see must not reach the others through 0 * NaN: it is taken out
+  // here and put back after the products, row by row.  Returns whether V held one.
+  static __device__ __forceinline__ bool widen(Bytes& b, u32x4* frags, int sub, bool mask, int key0, int any_from,
+                                               int last_pos) {
+    const int lane = (int)threadIdx.x & 63, g = lane >> 4;
+    bool has = false;
+    if (mask) {
+      const int from = seldom(key0 + sub * 16);
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        const int key = from + 4 * g + i;
+        const bool seen = key >= any_from && key <= last_pos;
+#pragma unroll
+        for (int w = 0; w < VB / 4; w++) {
+          const uint32_t v = seen ? b.v[i].v[w] : 0u;
+          const uint32_t hit = ((v & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+          has |= hit != 0;
+          b.v[i].v[w] = v & ~((hit >> 7) * 0xffu);
+        }
+      }
+    }
+    u32x4* kf = frags + ((sub >> 1) * 2 * kFrags + (sub & 1) * (DP / 32)) * 64 + lane;
+#pragma unroll
+    for (int j = 0; j < DP / 64; j++) {
+      kf[(2 * j) * 64] = widen8<BF16>(b.k[j][0], b.k[j][1]);
+      kf[(2 * j + 1) * 64] = widen8<BF16>(b.k[j][2], b.k[j][3]);
+    }
+    u32x2* vf = reinterpret_cast<u32x2*>(frags + ((sub >> 1) * 2 + 1) * kFrags * 64 + lane) + (sub & 1);
+#pragma unroll
+    for (int w = 0; w < VB / 4; w++) {
+      u32x2 e[4];
+#pragma unroll
+      for (int p = 0; p < 2; p++) {
+        uint32_t w0, w1, w2, w3;
+        zip2(b.v[2 * p].v[w], b.v[2 * p + 1].v[w], w0, w1, w2, w3);
+        e[0][p] = w0;
+        e[1][p] = w1;
+        e[2][p] = w2;
+        e[3][p] = w3;
+      }
+#pragma unroll
+      for (int j = 0; j < 4; j++) vf[(4 * w + j) * 128] = e[j];
+    }
+    return __ballot(has) != 0;
   }
 
   // Scores of 32 keys, whose operands begin at `at`, for the wave's rows.
@@ -115,8 +157,8 @@ struct Chunk {
   static __device__ __forceinline__ void run(const Args& a, const Seq& sq, const Task& task, int s, int h, int begin,
                                              int end, int part, float* lds) {
     const int tid = (int)threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), n = lane & 15, g = lane >> 4;
-    u32x4* const frags = reinterpret_cast<u32x4*>(lds);  // [32 keys][K, V][operand][lane]
-    int* const nan_word = reinterpret_cast<int*>(lds + kTile / 32 * 2 * kFrags * 256);
+    u32x4* const bufs = reinterpret_cast<u32x4*>(lds);  // two tiles: [32 keys][K, V][operand][lane]
+    int* const nan_words = reinterpret_cast<int*>(lds + 2 * kBuf * 4);
     const int32_t* table = a.table + s * a.table_row;
     const int row0 = task.r0 + wave * 16 * R;
 
@@ -156,65 +198,35 @@ struct Chunk {
     const int all_from = a.window > 0 ? max(task.last_pos - a.window + 1, 0) : 0;
     const int any_from = a.window > 0 ? max(task.first_pos - a.window + 1, 0) : 0;
 
+    const auto is_partial = [&](int tile) { return tile * kTile < all_from || (tile + 1) * kTile - 1 > task.first_pos; };
+    const auto bring = [&](Bytes& b, int tile) {
+      const int i = (tile - begin) & 1;
+      if (widen(b, bufs + i * kBuf, wave, is_partial(tile), tile * kTile, any_from, task.last_pos) && lane == 0)
+        nan_words[i] = tile;
+    };
+
+    // Tile i is used from one half of LDS while tile i + 1 is widened into the
+    // other and the bytes of tile i + 2 are on their way.
     Pages pages = load_pages(a, table, h, begin, task.last_pos), next_pages = pages;
-    Bytes raw = load(a, pages, 0);
+    Bytes raw = load(a, at_of(pages, wave));
+    bring(raw, begin);
+    if (begin + 1 < end) raw = load(a, at_of(pages, kSubs + wave));
+    meet();
     for (int tile = begin; tile < end; tile++) {
-      const int base = ((tile - begin) & 7) * kSubs;
+      const int i = tile - begin, base = (i & 7) * kSubs;
       const int key0 = tile * kTile;
-      const bool partial = key0 < all_from || key0 + kTile - 1 > task.first_pos;
-      meet();  // the last tile has been read
-      // ---- this wave's sub-tiles into LDS: operands of K, halves of operands of V ----
-      if (partial) {
-        const int from = seldom(key0);
-        bool has = false;
-#pragma unroll
-        for (int t = 0; t < kOwn; t++)
-#pragma unroll
-          for (int i = 0; i < 4; i++) {
-            const int key = from + (wave * kOwn + t) * 16 + 4 * g + i;
-            const bool seen = key >= any_from && key <= task.last_pos;
-#pragma unroll
-            for (int w = 0; w < VB / 4; w++) {
-              const uint32_t v = seen ? raw.v[t][i].v[w] : 0u;
-              const uint32_t hit = ((v & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-              has |= hit != 0;
-              raw.v[t][i].v[w] = v & ~((hit >> 7) * 0xffu);
-            }
-          }
-        if (__ballot(has) && lane == 0) *nan_word = tile;
-      }
-#pragma unroll
-      for (int t = 0; t < kOwn; t++) {
-        const int sub = wave * kOwn + t;
-        u32x4* kf = frags + ((sub >> 1) * 2 * kFrags + (sub & 1) * (DP / 32)) * 64 + lane;
-#pragma unroll
-        for (int j = 0; j < DP / 64; j++) {
-          kf[(2 * j) * 64] = widen8<BF16>(raw.k[t][j][0], raw.k[t][j][1]);
-          kf[(2 * j + 1) * 64] = widen8<BF16>(raw.k[t][j][2], raw.k[t][j][3]);
-        }
-        u32x2* vf = reinterpret_cast<u32x2*>(frags + ((sub >> 1) * 2 + 1) * kFrags * 64 + lane) + (sub & 1);
-#pragma unroll
-        for (int w = 0; w < VB / 4; w++) {
-          u32x2 e[4];
-#pragma unroll
-          for (int p = 0; p < 2; p++) {
-            uint32_t w0, w1, w2, w3;
-            zip2(raw.v[t][2 * p].v[w], raw.v[t][2 * p + 1].v[w], w0, w1, w2, w3);
-            e[0][p] = w0;
-            e[1][p] = w1;
-            e[2][p] = w2;
-            e[3][p] = w3;
-          }
-#pragma unroll
-          for (int j = 0; j < 4; j++) vf[(4 * w + j) * 128] = e[j];
-        }
-      }
+      const bool partial = is_partial(tile);
+      const u32x4* const frags = bufs + (i & 1) * kBuf;
+      const bool nan_v = partial && nan_words[i & 1] == tile;
       if (tile + 1 < end) {
-        if (((tile + 1 - begin) & 7) == 0) next_pages = load_pages(a, table, h, tile + 1, task.last_pos);
-        raw = load(a, next_pages, ((tile + 1 - begin) & 7) * kSubs);
+        bring(raw, tile + 1);
+        if (tile + 2 < end) {
+          if (((i + 2) & 7) == 0) next_pages = load_pages(a, table, h, tile + 2, task.last_pos);
+          const int64_t at = ((i + 2) >> 3) == (i >> 3) ? at_of(pages, ((i + 2) & 7) * kSubs + wave)
+                                                        : at_of(next_pages, ((i + 2) & 7) * kSubs + wave);
+          raw = load(a, at);
+        }
       }
-      meet();  // the tile is there
-      const bool nan_v = partial && *nan_word == tile;
 
       const float vmax = lane_of(pages.vmax, base);
       if (vmax > vref) {
@@ -352,10 +364,11 @@ struct Chunk {
           }
         }
       }
-      if (((tile + 1 - begin) & 7) == 0) {
+      if (((i + 1) & 7) == 0) {
         pages = next_pages;
         relative(pages, vref);
       }
+      meet();
     }
 
     // ---- a lane holds elements 4g VB .. 4g VB + 4 VB - 1 of its row ----
@@ -391,25 +404,33 @@ struct Chunk {
   }
 };
 
-}  // namespace
 
-// The workspace does not depend on FULL.
-uint64_t attention_chunk_workspace_bytes(int64_t dim) {
-  return dim <= 64 ? workspace_bytes<Chunk<true, 64, 4, 2, true>>() : workspace_bytes<Chunk<true, 128, 4, 2, true>>();
-}
+// Rows of a wave in sixteens, by the rows a sequence has on average: a task of
+// 256 rows would be half empty below 128.
+int wave_rows(int64_t T, int64_t S, int64_t group) { return T * group <= 128 * S ? 1 : 2; }
 
-namespace {
-template <bool BF16>
+template <bool BF16, int R>
 hipError_t by_dim(Args& a, void* ws, uint64_t ws_bytes, hipStream_t s) {
-  if (a.D == 64) return go<Chunk<BF16, 64, 4, 2, true>>(a, ws, ws_bytes, s);
-  if (a.D == 128) return go<Chunk<BF16, 128, 4, 2, true>>(a, ws, ws_bytes, s);
-  if (a.D < 64) return go<Chunk<BF16, 64, 4, 2, false>>(a, ws, ws_bytes, s);
-  return go<Chunk<BF16, 128, 4, 2, false>>(a, ws, ws_bytes, s);
+  if (a.D == 64) return go<Chunk<BF16, 64, R, true>>(a, ws, ws_bytes, s);
+  if (a.D == 128) return go<Chunk<BF16, 128, R, true>>(a, ws, ws_bytes, s);
+  if (a.D < 64) return go<Chunk<BF16, 64, R, false>>(a, ws, ws_bytes, s);
+  return go<Chunk<BF16, 128, R, false>>(a, ws, ws_bytes, s);
 }
+template <bool BF16>
+hipError_t by_rows(Args& a, void* ws, uint64_t ws_bytes, hipStream_t s) {
+  return wave_rows(a.T, a.S, a.group) == 1 ? by_dim<BF16, 1>(a, ws, ws_bytes, s) : by_dim<BF16, 2>(a, ws, ws_bytes, s);
+}
+
 }  // namespace
+
+uint64_t attention_chunk_workspace_bytes(int64_t T, int64_t S, int64_t group, int64_t dim) {
+  if (wave_rows(T, S, group) == 1)
+    return dim <= 64 ? workspace_bytes<Chunk<true, 64, 1, true>>() : workspace_bytes<Chunk<true, 128, 1, true>>();
+  return dim <= 64 ? workspace_bytes<Chunk<true, 64, 2, true>>() : workspace_bytes<Chunk<true, 128, 2, true>>();
+}
 
 hipError_t launch_attention_chunk(bool bf16, Args& a, void* ws, uint64_t ws_bytes, hipStream_t s) {
-  return bf16 ? by_dim<true>(a, ws, ws_bytes, s) : by_dim<false>(a, ws, ws_bytes, s);
+  return bf16 ? by_rows<true>(a, ws, ws_bytes, s) : by_rows<false>(a, ws, ws_bytes, s);
 }
 
 }  // namespace patch

@@ -505,7 +505,7 @@ hipError_t go(Args& a, void* ws, uint64_t ws_bytes, hipStream_t s) {
 }  // namespace attn
 
 // attention_chunk.hip
-uint64_t attention_chunk_workspace_bytes(int64_t dim);
+uint64_t attention_chunk_workspace_bytes(int64_t T, int64_t S, int64_t group, int64_t dim);
 hipError_t launch_attention_chunk(bool bf16, attn::Args& a, void* ws, uint64_t ws_bytes, hipStream_t s);
 
 }  // namespace patch
