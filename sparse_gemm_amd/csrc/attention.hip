@@ -316,7 +316,7 @@ struct Few {
   static constexpr int kLds = kWaves * kRows * (DP + 4) + kWaves * kRows * 2 + kWaves;
 
   static __device__ __forceinline__ void run(const Args& a, const Seq& sq, const Task& task, int s, int h, int begin,
-                                          int end, int part, float* lds) {
+                                             int end, const Part& part, float* lds) {
   constexpr int kLd = DP + 4, VB = DP / 16;
   const int tid = (int)threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), n = lane & 15,
             g = lane >> 4;
@@ -361,7 +361,7 @@ struct Few {
   __syncthreads();
 
   const int chunks = a.D / 8;
-  float* slot = a.parts + (int64_t)part * (kRows * (DP + 2));
+  float* slot = a.parts + part.slot((int)blockIdx.x - part.w0) * (kRows * (DP + 2));
   const __amdgpu_buffer_rsrc_t rs = rsrc(slot, kRows * (DP + 2) * 4);
   for (int e = tid; e < (task.r1 - task.r0) * chunks; e += kThreads) {
     const int row = e / chunks, d = (e - row * chunks) * 8;
@@ -383,7 +383,7 @@ struct Few {
 #pragma unroll
       for (int i = 0; i < 8; i++) acc[i] += fo * p[i];
     }
-    if (part < 0) {
+    if (part.count == 1) {
       store8<BF16>(a, out_at(a, sq, h, task.r0 + row, d), acc);
       if (a.lse && d == 0) store_lse(a, sq, h, task.r0 + row, lse_of(mx, sum));
     } else {

@@ -155,7 +155,7 @@ struct Chunk {
   }
 
   static __device__ __forceinline__ void run(const Args& a, const Seq& sq, const Task& task, int s, int h, int begin,
-                                             int end, int part, float* lds) {
+                                             int end, const Part& part, float* lds) {
     const int tid = (int)threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), n = lane & 15, g = lane >> 4;
     u32x4* const bufs = reinterpret_cast<u32x4*>(lds);  // two tiles: [32 keys][K, V][operand][lane]
     int* const nan_words = reinterpret_cast<int*>(lds + 2 * kBuf * 4);
@@ -276,8 +276,8 @@ struct Chunk {
           float mt[2];
 #pragma unroll
           for (int t = 0; t < 2; t++)
-            mt[t] = max3(max3(cur[r][t][0], cur[r][t][1], cur[r][t][2]), cur[r][t][3], cur[r][t][3]) * ks[t];
-          mx[r] = max3(mt[0], mt[1], mt[1]);
+            mt[t] = fmaxf(fmaxf(cur[r][t][0], cur[r][t][1]), fmaxf(cur[r][t][2], cur[r][t][3])) * ks[t];
+          mx[r] = fmaxf(mt[0], mt[1]);
           grows |= mx[r] > m[r] + kSlack;
         }
         if (__ballot(grows)) {
@@ -372,18 +372,22 @@ struct Chunk {
     }
 
     // ---- a lane holds elements 4g VB .. 4g VB + 4 VB - 1 of its row ----
-    float* slot = a.parts + (int64_t)part * (kRows * (DP + 2));
-    const __amdgpu_buffer_rsrc_t rs = rsrc(slot, kRows * (DP + 2) * 4);
+    const int me = (int)blockIdx.x - part.w0;
+    const bool store = part.count == 1;
+    const __amdgpu_buffer_rsrc_t rs = rsrc(a.parts + part.slot(me) * (kRows * (DP + 2)), kRows * (DP + 2) * 4);
 #pragma unroll
     for (int r = 0; r < R; r++) {
-      l[r] = quad_sum(l[r]);
       const int row = (wave * R + r) * 16 + n;  // of the task
+      l[r] = quad_sum(l[r]);
       if (task.r0 + row >= task.r1) continue;
       const float by = l[r] == 0.f || vref <= kNoScale ? 0.f : exp2_(vref) / l[r];
-      if (a.lse && g == 0 && part < 0) store_lse(a, sq, h, task.r0 + row, lse_of(m[r], l[r]));
-      if (part >= 0 && g == 0) {
-        const u32x2 ml = {__float_as_uint(m[r]), __float_as_uint(l[r])};
-        __builtin_amdgcn_raw_buffer_store_b64(ml, rs, (kRows * DP + 2 * row) * 4, 0, kCoherent);
+      if (g == 0) {
+        if (store) {
+          if (a.lse) store_lse(a, sq, h, task.r0 + row, lse_of(m[r], l[r]));
+        } else {
+          const u32x2 ml = {__float_as_uint(m[r]), __float_as_uint(l[r])};
+          __builtin_amdgcn_raw_buffer_store_b64(ml, rs, (kRows * DP + 2 * row) * 4, 0, kCoherent);
+        }
       }
 #pragma unroll
       for (int e = 0; e < 4 * VB; e += 8) {
@@ -392,7 +396,7 @@ struct Chunk {
         float v[8];
 #pragma unroll
         for (int i = 0; i < 8; i++) v[i] = o[r][(e + i) % VB][(e + i) / VB] * by;
-        if (part < 0) {
+        if (store) {
           store8<BF16>(a, out_at(a, sq, h, task.r0 + row, d), v);
         } else {
           const f32x4 v0 = {v[0], v[1], v[2], v[3]}, v1 = {v[4], v[5], v[6], v[7]};

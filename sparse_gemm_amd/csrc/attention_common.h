@@ -6,9 +6,9 @@
 //   kBf16, kWaves (of a workgroup), kDim (elements of a head, padded), kRows (of a task), kStep (keys of
 //   a step), kMinSteps (of a workgroup, at least), kTaskCost (what a task costs
 //   beside its steps, in steps), kPerCu (workgroups a CU), kLds (its LDS, floats),
-//   run(a, sq, task, s, h, begin, end, part, lds): the steps begin .. end - 1;
-//   with part < 0 they are all of the task's and the rows are stored, else o /
-//   l, m and l go to slot `part` of the workspace.
+//   run(a, sq, task, s, h, begin, end, part, lds): the steps begin .. end - 1.
+//   Of a task in one part the rows are stored, else o / l, m and l go to this
+//   workgroup's slot of the workspace.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -75,13 +75,6 @@ __device__ __forceinline__ u32x4 widen8(uint32_t lo, uint32_t hi) {
 __device__ __forceinline__ int seldom(int x) {
   asm volatile("" : "+v"(x));
   return x;
-}
-
-// Without the quieting of NaN operands that fmaxf's definition asks for.
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float r;
-  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
-  return r;
 }
 
 // The largest of a row's four lanes (16 apart), and their sum.  A swap of two
@@ -162,26 +155,56 @@ __device__ __forceinline__ Task task_of(const Args& a, const Seq& sq, int rt) {
   t.end = t.fill ? 1 : t.last_pos / Body::kStep + 1;
   return t;
 }
-// A head's cost on the line: its tasks' steps, and Body::kTaskCost for each task.
+// What a task takes of a line: `even`, the pieces it makes at kMinSteps or more
+// steps each; else its steps and kTaskCost.
 template <class Body>
-__device__ __forceinline__ int cost_of(const Args& a, const Seq& sq) {
-  const int tiles = (sq.n * a.group + Body::kRows - 1) / Body::kRows;
+__device__ __forceinline__ int size_of(const Task& t, bool even) {
+  const int steps = t.end - t.begin;
+  return even ? (steps + Body::kMinSteps - 1) / Body::kMinSteps : steps + Body::kTaskCost;
+}
+template <class Body>
+__device__ __forceinline__ int tiles_of(const Args& a, const Seq& sq) {
+  return (sq.n * a.group + Body::kRows - 1) / Body::kRows;
+}
+// Of a head's tasks together, by one lane.
+template <class Body>
+__device__ __forceinline__ int head_size(const Args& a, const Seq& sq, bool even) {
+  const int tiles = tiles_of<Body>(a, sq);
   int n = 0;
-  for (int i = 0; i < tiles; i++) {
-    const Task t = task_of<Body>(a, sq, i);
-    n += t.end - t.begin + Body::kTaskCost;
-  }
+  for (int i = 0; i < tiles; i++) n += size_of<Body>(task_of<Body>(a, sq, i), even);
   return n;
 }
-// The pieces a head's tasks make at Body::kMinSteps or more steps each.
+
+// Sums over the lanes before this one, and this one's own with them.
+__device__ __forceinline__ int wave_scan(int v) {
+  const int lane = (int)threadIdx.x & 63;
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const int x = __shfl_up(v, d);
+    if (lane >= d) v += x;
+  }
+  return v;
+}
+
+// The task at place u of a head's tasks (0 <= u < head_size), and where it
+// begins: 64 tasks at a time, one a lane.
 template <class Body>
-__device__ __forceinline__ int pieces_of(const Task& t) { return (t.end - t.begin + Body::kMinSteps - 1) / Body::kMinSteps; }
-template <class Body>
-__device__ __forceinline__ int pieces_of(const Args& a, const Seq& sq) {
-  const int tiles = (sq.n * a.group + Body::kRows - 1) / Body::kRows;
-  int n = 0;
-  for (int i = 0; i < tiles; i++) n += pieces_of<Body>(task_of<Body>(a, sq, i));
-  return n;
+__device__ __forceinline__ Task find_task(const Args& a, const Seq& sq, bool even, int u, int& at) {
+  const int tiles = tiles_of<Body>(a, sq), lane = (int)threadIdx.x & 63;
+  at = 0;
+  if (tiles == 1) return task_of<Body>(a, sq, 0);
+  for (int i0 = 0;; i0 += 64) {
+    const int i = i0 + lane;
+    const int n = i < tiles ? size_of<Body>(task_of<Body>(a, sq, i), even) : 0;
+    const int upto = wave_scan(n);
+    const uint64_t past = __ballot(at + upto > u);
+    if (past || i0 + 64 >= tiles) {
+      const int l = past ? __builtin_ctzll(past) : 0;
+      at += lane_of(upto - n, l);
+      return task_of<Body>(a, sq, i0 + l);
+    }
+    at += lane_of(upto, 63);
+  }
 }
 
 // Eight neighbouring outputs.
@@ -234,32 +257,58 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void* p, uint32_t b
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, (int)bytes, 0x00020000);
 }
 
-// Join the parts of a task: slot 1 of worker w0, then slot 0 of the next.
+// A task's parts: part p of `count` by workgroup w0 + p, part 0 in slot 1 of
+// its workgroup, the others in slot 0.
+struct Part {
+  int w0, count;
+  __device__ __forceinline__ int64_t slot(int p) const { return 2 * ((int64_t)w0 + p) + (p == 0); }
+};
+
+// Whether the flags of all parts are set; if so they are put back.  By the
+// whole workgroup, with a word of LDS that is not in use.
+__device__ __forceinline__ bool all_there(const Args& a, const Part& part, int* word) {
+  if (threadIdx.x < 64) {
+    bool all = true;
+    for (int p = (int)threadIdx.x; p < part.count; p += 64)
+      all &= __hip_atomic_load(a.flags + part.slot(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == a.token;
+    const bool done = __ballot(!all) == 0;
+    if (threadIdx.x == 0) *word = done;
+    if (done)
+      for (int p = (int)threadIdx.x; p < part.count; p += 64)
+        __hip_atomic_store(a.flags + part.slot(p), (uint64_t)0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  __syncthreads();
+  return *word != 0;
+}
+
+// Join the parts of a task and store its rows.
 template <class Body>
-__device__ __forceinline__ void join_parts(const Args& a, const Seq& sq, const Task& task, int h, int w0, int count) {
+__device__ __forceinline__ void join_parts(const Args& a, const Seq& sq, const Task& task, int h, const Part& part) {
   constexpr int kRows = Body::kRows, DP = Body::kDim, kSlot = kRows * (DP + 2);
   const int chunks = a.D / 8;
   for (int e = threadIdx.x; e < (task.r1 - task.r0) * chunks; e += threads_of<Body>) {
     const int row = e / chunks, d = (e - row * chunks) * 8;
     float mx = -kInf, sum = 0.f, acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-    for (int p = 0; p < count; p++) {
-      const int64_t slot = 2 * ((int64_t)w0 + p) + (p == 0);
-      const __amdgpu_buffer_rsrc_t rs = rsrc(a.parts + slot * kSlot, kSlot * 4);
+    const auto load = [&](int p, float& m, float& l, f32x4& lo, f32x4& hi) {
+      const __amdgpu_buffer_rsrc_t rs = rsrc(a.parts + part.slot(p) * kSlot, kSlot * 4);
       const int at = (row * DP + d) * 4;
       const u32x2 ml = __builtin_amdgcn_raw_buffer_load_b64(rs, (kRows * DP + 2 * row) * 4, 0, kCoherent);
-      const f32x4 lo = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, at, 0, kCoherent));
-      const f32x4 hi = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, at + 16, 0, kCoherent));
-      const float m = __uint_as_float(ml[0]), l = __uint_as_float(ml[1]);
+      lo = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, at, 0, kCoherent));
+      hi = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, at + 16, 0, kCoherent));
+      m = __uint_as_float(ml[0]);
+      l = __uint_as_float(ml[1]);
+    };
+#pragma unroll 4
+    for (int p = 0; p < part.count; p++) {
+      float m, l;
+      f32x4 x[2];
+      load(p, m, l, x[0], x[1]);
       const float mn = fmaxf(mx, m), mu = finite_or_0(mn);
       const float f = exp2_(mx - mu), w = exp2_(m - mu) * l;
       mx = mn;
       sum = sum * f + w;
 #pragma unroll
-      for (int i = 0; i < 4; i++) {
-        acc[i] = acc[i] * f + w * lo[i];
-        acc[4 + i] = acc[4 + i] * f + w * hi[i];
-      }
+      for (int i = 0; i < 8; i++) acc[i] = acc[i] * f + w * x[i / 4][i % 4];
     }
     const float inv = sum == 0.f ? 0.f : 1.0f / sum;
 #pragma unroll
@@ -277,14 +326,7 @@ struct Place {
 // A line over up to 64 sequences, one a lane; every wave has its own.
 struct LaneLine {
   int from, to, total;
-  __device__ __forceinline__ explicit LaneLine(int n) {
-    const int lane = (int)threadIdx.x & 63;
-    to = n;
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-      const int v = __shfl_up(to, d);
-      if (lane >= d) to += v;
-    }
+  __device__ __forceinline__ explicit LaneLine(int n) : to(wave_scan(n)) {
     from = to - n;
     total = lane_of(to, 63);
   }
@@ -308,12 +350,7 @@ struct LdsLine {
       line[s] = cost(s);
       mine += line[s];
     }
-    int upto = mine;
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-      const int v = __shfl_up(upto, d);
-      if (lane >= d) upto += v;
-    }
+    const int upto = wave_scan(mine);
     if (lane == 63) wave_sum[wave] = upto;
     __syncthreads();
     int at = upto - mine;
@@ -336,43 +373,36 @@ struct LdsLine {
   }
 };
 
-// Steps begin .. end - 1 of a task by this workgroup, one of the task's
-// `count` parts, which the workgroups w0 .. w0 + count - 1 have: part 0 in
-// slot 1 of its workgroup, the others in slot 0.
+// n places in `pieces` pieces that differ by one at most, the longer ones first.
+struct Cut {
+  int pieces, each, more;
+  __device__ __forceinline__ Cut(int n, int p) : pieces(p), each(p > 0 ? n / p : 0), more(p > 0 ? n - each * p : 0) {}
+  __device__ __forceinline__ int start(int i) const { return i * each + min(i, more); }
+  __device__ __forceinline__ int piece(int u) const {  // the piece of place u
+    const int longer = more * (each + 1);
+    return u < longer ? u / (each + 1) : more + (u - longer) / max(each, 1);
+  }
+};
+
+// Steps begin .. end - 1 of a task by this workgroup.
 template <class Body>
 __device__ __forceinline__ void run_piece(const Args& a, const Seq& sq, const Task& task, int s, int h, int begin,
-                                          int end, int w0, int count, float* lds, int* joined) {
+                                          int end, const Part& part, float* lds, int* joined) {
   if (task.fill) {
     fill_rows<Body>(a, sq, task, h);
     return;
   }
-  const int lane = (int)threadIdx.x & 63;
-  const int mine = count == 1 ? -1 : 2 * (int)blockIdx.x + ((int)blockIdx.x == w0 ? 1 : 0);
-  Body::run(a, sq, task, s, h, begin, end, mine, lds);
-  if (count > 1) {
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's share of the part has arrived
-    __syncthreads();
-    if (threadIdx.x < 64) {
-      if (lane == 0) {
-        const uint64_t old =
-            __hip_atomic_exchange(a.flags + mine, a.token, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        asm volatile("" ::"v"(old));
-      }
-      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // and its flag, before the others' are read
-      bool all = true;
-      for (int p = lane; p < count; p += 64)
-        all &= __hip_atomic_load(a.flags + 2 * (w0 + p) + (p == 0), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
-               a.token;
-      const bool done = __ballot(!all) == 0;
-      if (lane == 0) *joined = done;
-      if (done)
-        for (int p = lane; p < count; p += 64)
-          __hip_atomic_store(a.flags + 2 * (w0 + p) + (p == 0), (uint64_t)0, __ATOMIC_RELAXED,
-                             __HIP_MEMORY_SCOPE_AGENT);
-    }
-    __syncthreads();
-    if (*joined) join_parts<Body>(a, sq, task, h, w0, count);
+  Body::run(a, sq, task, s, h, begin, end, part, lds);
+  if (part.count == 1) return;
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's share of them has arrived
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    const uint64_t old = __hip_atomic_exchange(a.flags + part.slot((int)blockIdx.x - part.w0), a.token, __ATOMIC_RELAXED,
+                                               __HIP_MEMORY_SCOPE_AGENT);
+    asm volatile("" ::"v"(old));
   }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // and the flag, before the others' are read
+  if (all_there(a, part, joined)) join_parts<Body>(a, sq, task, h, part);
 }
 
 // All work on one line (see the top).  Where there are fewer pieces of
@@ -393,50 +423,60 @@ __global__ __launch_bounds__(threads_of<Body>, Body::kPerCu* Body::kWaves / 4) v
     return MANY ? seq_of(a, s)
                 : Seq{lane_of(mine.c0, s), lane_of(mine.n, s), lane_of(mine.past, s), lane_of((int)mine.bad, s) != 0};
   };
-  const auto make = [&](auto f) {  // a line of f(sequence) for every head
-    if constexpr (MANY)
+  const auto make = [&](bool even) {
+    if constexpr (MANY) {
       return LdsLine<Body>(a.S, reinterpret_cast<int*>(lds + Body::kLds), wave_sum,
-                     [&](int s) { return f(seq_of(a, s)) * a.kv_heads; });
-    else
-      return LaneLine(lane < a.S ? f(mine) * a.kv_heads : 0);
+                           [&](int s) { return head_size<Body>(a, seq_of(a, s), even) * a.kv_heads; });
+    } else {
+      int n = 0;
+      if (__ballot(tiles_of<Body>(a, mine) > 2) == 0) {
+        n = head_size<Body>(a, mine, even);
+      } else {  // a sequence at a time, a task a lane
+        for (int s = 0; s < a.S; s++) {
+          const Seq sq = seq_at(s);
+          const int tiles = tiles_of<Body>(a, sq);
+          int x = 0;
+          for (int i = lane; i < tiles; i += 64) x += size_of<Body>(task_of<Body>(a, sq, i), even);
+          x = lane_of(wave_scan(x), 63);
+          if (lane == s) n = x;
+        }
+      }
+      return LaneLine(n * a.kv_heads);
+    }
   };
-  auto line = make([&](const Seq& q) { return pieces_of<Body>(a, q); });
+  auto line = make(true);
   const bool even = line.total <= (int)gridDim.x;  // a piece a workgroup
-  if (!even) line = make([&](const Seq& q) { return cost_of<Body>(a, q); });
-  const int per = even ? 1 : (line.total + (int)gridDim.x - 1) / (int)gridDim.x;
-  int u = per * (int)blockIdx.x;
-  const int u_end = min(u + per, line.total);
+  if (!even) line = make(false);
+  const Cut cut(line.total, even ? line.total : (int)gridDim.x);
+  if ((int)blockIdx.x >= cut.pieces) return;
+  int u = cut.start((int)blockIdx.x);
+  const int u_end = cut.start((int)blockIdx.x + 1);
   while (u < u_end) {
     const Place pl = line.find(u);
     const Seq sq = seq_at(pl.s);
     const int per_head = (pl.to - pl.from) / a.kv_heads, h = (u - pl.from) / per_head;
-    int at = pl.from + h * per_head, rt = 0;  // where the task begins on the line
-    Task task = task_of<Body>(a, sq, 0);
-    int size = even ? pieces_of<Body>(task) : task.end - task.begin + kTaskCost;
-    while (at + size <= u) {
-      at += size;
-      task = task_of<Body>(a, sq, ++rt);
-      size = even ? pieces_of<Body>(task) : task.end - task.begin + kTaskCost;
-    }
-    int begin, end, w0, count;
+    int at;  // where the task begins on the line
+    const Task task = find_task<Body>(a, sq, even, u - pl.from - h * per_head, at);
+    at += pl.from + h * per_head;
+    const int steps = task.end - task.begin, size = size_of<Body>(task, even);
+    int begin, end;
+    Part part;
     if (even) {
-      const int steps = task.end - task.begin, i = u - at;
-      const int each = steps / size, more = steps - each * size;  // the first `more` pieces have one step more
-      begin = task.begin + i * each + min(i, more);
-      end = begin + each + (i < more ? 1 : 0);
-      w0 = at;
-      count = size;
+      const Cut of(steps, size);
+      begin = task.begin + of.start(u - at);
+      end = task.begin + of.start(u - at + 1);
+      part = Part{at, size};
       u = u_end;
     } else {
       const int first = at + kTaskCost, last = at + size;  // the task's steps on the line
       begin = task.begin + max(u - first, 0);
       end = task.begin + min(u_end, last) - first;
-      w0 = first / per;
-      count = (last - 1) / per - w0 + 1;
+      part.w0 = cut.piece(first);
+      part.count = cut.piece(last - 1) - part.w0 + 1;
       u = last;
     }
     if (begin < end) {
-      run_piece<Body>(a, sq, task, pl.s, h, begin, end, w0, count, lds, &joined);
+      run_piece<Body>(a, sq, task, pl.s, h, begin, end, part, lds, &joined);
       __syncthreads();  // LDS is used again
     }
   }
@@ -459,7 +499,7 @@ __global__ __launch_bounds__(threads_of<Body>, Body::kPerCu* Body::kWaves / 4) v
   if (task.fill)
     fill_rows<Body>(a, sq, task, h);
   else
-    Body::run(a, sq, task, s, h, task.begin, task.end, -1, lds);
+    Body::run(a, sq, task, s, h, task.begin, task.end, Part{0, 1}, lds);
 }
 
 // ---- launch ----
