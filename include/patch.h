@@ -616,14 +616,14 @@ patch_status patch_attention(const patch_attention_args* args, const patch_kv_ca
  * packed_dev: per band of 16 rows, first the weights of 128 columns at a time
  * (1 KB: lane l's 16 bytes at 16 l, row l % 16; its 32-bit word j holds the
  * columns 32 j + 8 (l / 16) .. + 7, column 2i in bits 4i.., 2i + 1 in bits 16
- * + 4i..), K padded to 128; after all bands the scales, per band [group][16
- * rows] of dtype, then with zero the zeros likewise, a byte each.  Rows behind
- * N and columns behind K: zeros.
+ * + 4i..), K padded to 128; after all bands the scales of dtype, per band and
+ * 128 columns [4 quads of rows][group][4 rows], then with zero the zeros
+ * likewise, a byte each.  Rows behind N and columns behind K: zeros.
  *
  * patch_w4_gemm: X M x K of dtype (PATCH_F16, PATCH_BF16), Y M x N of y_dtype
  * (dtype or PATCH_F32), both contiguous.  Weights are exact in the matrix
  * instructions; sums are fp32, a group's sum multiplied by its scale in fp32.
- * Any M >= 0 runs; the weights are read once for every 64 rows of X, so many
+ * Any M >= 0 runs; the weights are read once for every 32 rows of X, so many
  * tokens are better served by the GEMMs above.
  * Errors: PATCH_ERR_SHAPE (sizes), PATCH_ERR_INVALID_ARG (null pointers,
  * misalignment, dtypes, M < 0), PATCH_ERR_BUFFER_TOO_SMALL (packed).

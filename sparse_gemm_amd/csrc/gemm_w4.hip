@@ -16,8 +16,9 @@
 //     cancellation costs three bits of an fp32 sum at most.
 //   * A band's weights lie in lane order (patch_w4_pack), 1 KB for 128 columns:
 //     one 16-byte load a lane feeds four matrix instructions.
-//   * A workgroup has one band of 16 rows; its waves take the 128-column blocks
-//     in turn and join their sums through LDS in a fixed order.
+//   * A workgroup has one or two bands of 16 rows; its waves take the 128-column
+//     blocks in turn, the next block's bytes on their way while one is used, and
+//     join their sums through LDS in a fixed order.
 #include <algorithm>
 
 #include "device_common.h"
@@ -26,7 +27,19 @@
 namespace patch {
 namespace {
 
-constexpr int kWaves = 8;
+#ifndef WB
+#define WB 2
+#endif
+#ifndef KWV
+#define KWV 8
+#endif
+constexpr int kMaxWaves = KWV;
+#ifndef RBMIN
+#define RBMIN 512
+#endif
+#ifndef RBX
+#define RBX 2
+#endif
 
 // The eight operand elements 16 + q of a packed word.
 template <bool BF16>
@@ -47,102 +60,133 @@ __device__ __forceinline__ u32x4 widen4(uint32_t w) {
 
 struct W4Args {
   const uint8_t* w;      // bands of blocks
-  const uint8_t* scale;  // [band][group][16] 16-bit
-  const uint8_t* zero;   // [band][group][16] bytes
+  const uint8_t* scale;  // [band][block][4 quads of rows][group][4 rows] 16-bit
+  const uint8_t* zero;   // likewise, bytes
   const void* X;
   void* Y;
   int64_t M, N, K;
-  int blocks;  // 128-column blocks of a band
-  int groups;  // groups of a row
+  int bands, blocks;  // of 16 rows, of 128 columns
+  int group;
 };
 
-// MT blocks of 16 tokens, G columns a group.
-template <bool BF16, bool OUT_F32, int MT, int G, bool ZERO>
-__global__ __launch_bounds__(kWaves * 64) void k_w4(W4Args a) {
-  __shared__ f32x4 part[kWaves][MT][64];
-  const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6, n = lane & 15, g = lane >> 4;
-  const int64_t band = blockIdx.x, m0 = (int64_t)blockIdx.y * (16 * MT);
-  const uint8_t* wp = a.w + (band * a.blocks) * 1024 + lane * 16;
-  const uint8_t* sp = a.scale + (band * a.groups * 16 + 4 * g) * 2;
-  const uint8_t* zp = ZERO ? a.zero + band * a.groups * 16 + 4 * g : nullptr;
-  const uint16_t* xp[MT];
+// The bytes of one 128-column block of RB bands and MT blocks of 16 tokens.
+template <int MT, int RB, int G, bool ZERO>
+struct Block {
+  static constexpr int kGroups = 128 / G;  // groups of a block
+  u32x4 w[RB];
+  Vec<uint32_t, 2 * kGroups> s[RB];  // four rows' scales, group by group
+  Vec<uint32_t, kGroups> z[RB];
+  u32x4 x[MT][4];
+};
+template <int MT, int RB, int G, bool ZERO>
+__device__ __forceinline__ Block<MT, RB, G, ZERO> load_block(const W4Args& a, int64_t band, const uint16_t* const (&xp)[MT],
+                                                             int b) {
+  using B = Block<MT, RB, G, ZERO>;
+  const int lane = (int)threadIdx.x & 63, g = lane >> 4;
+  B r;
+#pragma unroll
+  for (int i = 0; i < RB; i++) {
+    const int64_t at = min(band + i, (int64_t)a.bands - 1) * a.blocks + b;  // a band behind the last: not stored
+    r.w[i] = ld16(a.w + at * 1024 + lane * 16);
+    r.s[i] = *reinterpret_cast<const Vec<uint32_t, 2 * B::kGroups>*>(a.scale + (at * 4 + g) * (8 * B::kGroups));
+    if constexpr (ZERO)
+      r.z[i] = *reinterpret_cast<const Vec<uint32_t, B::kGroups>*>(a.zero + (at * 4 + g) * (4 * B::kGroups));
+  }
 #pragma unroll
   for (int t = 0; t < MT; t++)
-    xp[t] = reinterpret_cast<const uint16_t*>(a.X) + std::min(m0 + 16 * t + n, a.M - 1) * a.K;  // rows behind M: the last, not stored
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+      const int64_t k = (int64_t)b * 128 + 32 * j + 8 * g;
+      r.x[t][j] = ld16_pred(xp[t] + k, k < a.K);  // columns behind K are zeros in X too
+    }
+  return r;
+}
+
+template <bool BF16, int MT, int RB, int G, bool ZERO>
+__device__ __forceinline__ void multiply(const Block<MT, RB, G, ZERO>& b, f32x4 (&y)[RB][MT]) {
+  constexpr int kGroups = 128 / G, kJ = G / 32;  // instructions of a group
   const uint32_t one2 = BF16 ? 0x3f803f80u : 0x3c003c00u;
   const u32x4 ones = {one2, one2, one2, one2};
-  constexpr int kGroups = 128 / G;  // groups of a block
-  constexpr int kJ = G / 32;        // instructions of a group
-  f32x4 y[MT];
 #pragma unroll
-  for (int t = 0; t < MT; t++) y[t] = (f32x4){0.f, 0.f, 0.f, 0.f};
-
-  for (int b = wave; b < a.blocks; b += kWaves) {
-    const u32x4 w = ld16(wp + (int64_t)b * 1024);
-    u32x4 x[MT][4];
+  for (int q = 0; q < kGroups; q++) {
+    f32x4 sum[MT];
 #pragma unroll
-    for (int t = 0; t < MT; t++)
+    for (int t = 0; t < MT; t++) {
+      sum[t] = (f32x4){0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int j = 0; j < 4; j++) {
-        const int64_t k = (int64_t)b * 128 + 32 * j + 8 * g;
-        x[t][j] = ld16_pred(xp[t] + k, k < a.K);  // columns behind K are zeros in X too
-      }
+      for (int j = 0; j < kJ; j++) sum[t] = mma_dense<BF16>(ones, b.x[t][q * kJ + j], sum[t]);
+    }
 #pragma unroll
-    for (int q = 0; q < kGroups; q++) {
-      const int gr = b * kGroups + q;
-      if (gr >= a.groups) break;
-      const u32x2 s2 = *reinterpret_cast<const u32x2*>(sp + (int64_t)gr * 32);
+    for (int i = 0; i < RB; i++) {
       float s[4], z[4];
 #pragma unroll
-      for (int i = 0; i < 4; i++) {
-        const uint16_t h = (uint16_t)(s2[i >> 1] >> (16 * (i & 1)));
-        s[i] = BF16 ? __uint_as_float((uint32_t)h << 16) : (float)__builtin_bit_cast(_Float16, h);
+      for (int r = 0; r < 4; r++) {
+        const uint16_t h = (uint16_t)(b.s[i].v[2 * q + (r >> 1)] >> (16 * (r & 1)));
+        s[r] = BF16 ? __uint_as_float((uint32_t)h << 16) : (float)__builtin_bit_cast(_Float16, h);
+        z[r] = ZERO ? 16.0f + (float)((b.z[i].v[q] >> (8 * r)) & 15u) : 24.0f;
       }
-      if constexpr (ZERO) {
-        const uint32_t zw = *reinterpret_cast<const uint32_t*>(zp + (int64_t)gr * 16);
+      u32x4 w[kJ];
 #pragma unroll
-        for (int i = 0; i < 4; i++) z[i] = 16.0f + (float)((zw >> (8 * i)) & 15u);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; i++) z[i] = 24.0f;
-      }
-      u32x4 wq[kJ];
-#pragma unroll
-      for (int j = 0; j < kJ; j++) wq[j] = widen4<BF16>(w[q * kJ + j]);
+      for (int j = 0; j < kJ; j++) w[j] = widen4<BF16>(b.w[i][q * kJ + j]);
 #pragma unroll
       for (int t = 0; t < MT; t++) {
-        f32x4 acc = {0.f, 0.f, 0.f, 0.f}, sum = {0.f, 0.f, 0.f, 0.f};
+        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int j = 0; j < kJ; j++) {
-          acc = mma_dense<BF16>(wq[j], x[t][q * kJ + j], acc);
-          sum = mma_dense<BF16>(ones, x[t][q * kJ + j], sum);
-        }
+        for (int j = 0; j < kJ; j++) acc = mma_dense<BF16>(w[j], b.x[t][q * kJ + j], acc);
 #pragma unroll
-        for (int i = 0; i < 4; i++) y[t][i] += s[i] * (acc[i] - z[i] * sum[i]);
+        for (int r = 0; r < 4; r++) y[i][t][r] += s[r] * (acc[r] - z[r] * sum[t][r]);
       }
     }
   }
+}
+
+// MT blocks of 16 tokens, RB bands, G columns a group.
+template <bool BF16, bool OUT_F32, int MT, int RB, int G, bool ZERO>
+__global__ __launch_bounds__(kMaxWaves * 64) void k_w4(W4Args a) {
+  extern __shared__ f32x4 part[];  // [wave][RB][MT][lane]
+  const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6, waves = (int)blockDim.x >> 6, n = lane & 15;
+  const int64_t band = (int64_t)blockIdx.x * RB, m0 = (int64_t)blockIdx.y * (16 * MT);
+  const uint16_t* xp[MT];
 #pragma unroll
-  for (int t = 0; t < MT; t++) part[wave][t][lane] = y[t];
+  for (int t = 0; t < MT; t++)  // rows behind M: the last, not stored
+    xp[t] = reinterpret_cast<const uint16_t*>(a.X) + min(m0 + 16 * t + n, a.M - 1) * a.K;
+  f32x4 y[RB][MT];
+#pragma unroll
+  for (int i = 0; i < RB; i++)
+#pragma unroll
+    for (int t = 0; t < MT; t++) y[i][t] = (f32x4){0.f, 0.f, 0.f, 0.f};
+
+  if (wave < a.blocks) {
+    Block<MT, RB, G, ZERO> cur = load_block<MT, RB, G, ZERO>(a, band, xp, wave);
+    for (int b = wave; b < a.blocks; b += waves) {
+      // the next block's bytes are on their way while this one's are used
+      const Block<MT, RB, G, ZERO> next = load_block<MT, RB, G, ZERO>(a, band, xp, b + waves < a.blocks ? b + waves : b);
+      multiply<BF16, MT, RB, G, ZERO>(cur, y);
+      cur = next;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < RB; i++)
+#pragma unroll
+    for (int t = 0; t < MT; t++) part[((wave * RB + i) * MT + t) * 64 + lane] = y[i][t];
   __syncthreads();
   // lane l of block t holds rows 4 (l / 16) .. + 3, token l % 16
-  for (int e = (int)threadIdx.x; e < MT * 64; e += kWaves * 64) {
-    const int t = e >> 6, l = e & 63;
-    f32x4 v = part[0][t][l];
-#pragma unroll
-    for (int w = 1; w < kWaves; w++) v += part[w][t][l];
-    const int64_t m = m0 + 16 * t + (l & 15), row = band * 16 + 4 * (l >> 4);
+  for (int e = (int)threadIdx.x; e < RB * MT * 64; e += (int)blockDim.x) {
+    const int i = e / (MT * 64), t = (e >> 6) % MT, l = e & 63;
+    f32x4 v = part[e];
+    for (int w = 1; w < waves; w++) v += part[w * RB * MT * 64 + e];
+    const int64_t m = m0 + 16 * t + (l & 15), row = (band + i) * 16 + 4 * (l >> 4);
     if (m >= a.M || row >= a.N) continue;
     if (row + 4 <= a.N && (a.N & 3) == 0) {
       store4<BF16, OUT_F32>(a.Y, m * a.N + row, v);
     } else {
-      for (int i = 0; i < 4 && row + i < a.N; i++) {
+      for (int c = 0; c < 4 && row + c < a.N; c++) {
         if constexpr (OUT_F32)
-          reinterpret_cast<float*>(a.Y)[m * a.N + row + i] = v[i];
+          reinterpret_cast<float*>(a.Y)[m * a.N + row + c] = v[c];
         else if constexpr (BF16)
-          reinterpret_cast<__bf16*>(a.Y)[m * a.N + row + i] = (__bf16)v[i];
+          reinterpret_cast<__bf16*>(a.Y)[m * a.N + row + c] = (__bf16)v[c];
         else
-          reinterpret_cast<_Float16*>(a.Y)[m * a.N + row + i] = (_Float16)v[i];
+          reinterpret_cast<_Float16*>(a.Y)[m * a.N + row + c] = (_Float16)v[c];
       }
     }
   }
@@ -152,14 +196,16 @@ __global__ __launch_bounds__(kWaves * 64) void k_w4(W4Args a) {
 __host__ __device__ inline int64_t n_bands(int64_t N) { return (N + 15) / 16; }
 __host__ __device__ inline int64_t n_blocks(int64_t K) { return (K + 127) / 128; }
 inline int64_t scale_offset(int64_t N, int64_t K) { return n_bands(N) * n_blocks(K) * 1024; }
-inline int64_t zero_offset(int64_t N, int64_t K, int64_t G) { return scale_offset(N, K) + n_bands(N) * 16 * (K / G) * 2; }
+inline int64_t n_scales(int64_t N, int64_t K, int64_t G) { return n_bands(N) * 16 * n_blocks(K) * (128 / G); }
+inline int64_t zero_offset(int64_t N, int64_t K, int64_t G) { return scale_offset(N, K) + n_scales(N, K, G) * 2; }
 
 // One thread a 32-bit word of the weights, then one a scale and zero.
 __global__ __launch_bounds__(256) void k_w4_pack(int64_t N, int64_t K, int64_t G, const uint8_t* __restrict__ q,
                                                  const uint16_t* __restrict__ scale, const uint8_t* __restrict__ zero,
                                                  uint32_t* __restrict__ w, uint16_t* __restrict__ so,
                                                  uint8_t* __restrict__ zo) {
-  const int64_t words = n_bands(N) * n_blocks(K) * 256, groups = K / G, extra = n_bands(N) * groups * 16;
+  const int64_t words = n_bands(N) * n_blocks(K) * 256, groups = K / G, per = 128 / G;
+  const int64_t extra = n_bands(N) * 16 * n_blocks(K) * per;
   for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < words + extra; e += (int64_t)gridDim.x * 256) {
     if (e < words) {
       const int64_t block = e >> 8, band = block / n_blocks(K);
@@ -174,9 +220,13 @@ __global__ __launch_bounds__(256) void k_w4_pack(int64_t N, int64_t K, int64_t G
       }
       w[e] = v;
     } else {
-      const int64_t f = e - words, band = f / (groups * 16), r = f - band * groups * 16, gr = r >> 4, row = band * 16 + (r & 15);
-      so[f] = row < N ? scale[row * groups + gr] : (uint16_t)0;
-      if (zo) zo[f] = row < N ? zero[row * groups + gr] & 15 : 0;
+      // place f = (((band, block), quad), group of the block), row of the quad
+      const int64_t f = e - words, block = f / (16 * per), band = block / n_blocks(K);
+      const int r = (int)(f - block * 16 * per), quad = r / (4 * (int)per), c = r - quad * 4 * (int)per;
+      const int64_t row = band * 16 + 4 * quad + (c & 3), gr = (block - band * n_blocks(K)) * per + (c >> 2);
+      const bool ok = row < N && gr < groups;
+      so[f] = ok ? scale[row * groups + gr] : (uint16_t)0;
+      if (zo) zo[f] = ok ? zero[row * groups + gr] & 15 : 0;
     }
   }
 }
@@ -224,37 +274,40 @@ __global__ __launch_bounds__(256) void k_w4_quantize(int64_t N, int64_t K, int G
   }
 }
 
-template <bool BF16, bool OUT_F32, int MT, int G, bool ZERO>
+template <bool BF16, bool OUT_F32, int MT, int RB, int G, bool ZERO>
 hipError_t go(const W4Args& a, hipStream_t s) {
   const int64_t my = (a.M + 16 * MT - 1) / (16 * MT);
   if (my > 65535) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((k_w4<BF16, OUT_F32, MT, G, ZERO>), dim3((unsigned)n_bands(a.N), (unsigned)my), dim3(kWaves * 64), 0,
-                     s, a);
+  // a wave takes two blocks or more where there are enough
+  const int waves = std::max(1, std::min(kMaxWaves, a.blocks / WB));
+  const size_t lds = (size_t)waves * RB * MT * 1024;
+  hipLaunchKernelGGL((k_w4<BF16, OUT_F32, MT, RB, G, ZERO>), dim3((unsigned)((a.bands + RB - 1) / RB), (unsigned)my),
+                     dim3(64 * waves), lds, s, a);
   return hipGetLastError();
 }
-template <bool BF16, bool OUT_F32, int MT, int G>
+template <bool BF16, bool OUT_F32, int MT, int RB, int G>
 hipError_t by_zero(const W4Args& a, hipStream_t s) {
-  return a.zero ? go<BF16, OUT_F32, MT, G, true>(a, s) : go<BF16, OUT_F32, MT, G, false>(a, s);
+  return a.zero ? go<BF16, OUT_F32, MT, RB, G, true>(a, s) : go<BF16, OUT_F32, MT, RB, G, false>(a, s);
 }
-template <bool BF16, bool OUT_F32, int MT>
+template <bool BF16, bool OUT_F32, int MT, int RB>
 hipError_t by_group(const W4Args& a, hipStream_t s) {
-  switch (a.K / a.groups) {
-    case 32: return by_zero<BF16, OUT_F32, MT, 32>(a, s);
-    case 64: return by_zero<BF16, OUT_F32, MT, 64>(a, s);
-    default: return by_zero<BF16, OUT_F32, MT, 128>(a, s);
+  switch (a.group) {
+    case 32: return by_zero<BF16, OUT_F32, MT, RB, 32>(a, s);
+    case 64: return by_zero<BF16, OUT_F32, MT, RB, 64>(a, s);
+    default: return by_zero<BF16, OUT_F32, MT, RB, 128>(a, s);
   }
 }
 template <bool BF16, bool OUT_F32>
 hipError_t by_tokens(const W4Args& a, hipStream_t s) {
-  if (a.M <= 16) return by_group<BF16, OUT_F32, 1>(a, s);
-  if (a.M <= 32) return by_group<BF16, OUT_F32, 2>(a, s);
-  return by_group<BF16, OUT_F32, 4>(a, s);
+  // more than four tokens: X is most of what a wave reads, and two bands share it
+  if (a.M <= 16) return a.M > 4 && a.bands >= RBMIN ? by_group<BF16, OUT_F32, 1, RBX>(a, s) : by_group<BF16, OUT_F32, 1, 1>(a, s);
+  return by_group<BF16, OUT_F32, 2, 1>(a, s);
 }
 
 }  // namespace
 
 uint64_t w4_bytes(int64_t N, int64_t K, int64_t G, bool zero) {
-  return (uint64_t)(zero_offset(N, K, G) + (zero ? n_bands(N) * 16 * (K / G) : 0));
+  return (uint64_t)(zero_offset(N, K, G) + (zero ? n_scales(N, K, G) : 0));
 }
 
 hipError_t launch_w4_quantize(bool bf16, int64_t N, int64_t K, int group, const void* W, uint8_t* q, void* scale,
@@ -272,7 +325,7 @@ hipError_t launch_w4_quantize(bool bf16, int64_t N, int64_t K, int group, const 
 
 hipError_t launch_w4_pack(int64_t N, int64_t K, int group, const uint8_t* q, const void* scale, const uint8_t* zero,
                           uint8_t* packed, hipStream_t s) {
-  const int64_t all = n_bands(N) * n_blocks(K) * 256 + n_bands(N) * 16 * (K / group);
+  const int64_t all = n_bands(N) * n_blocks(K) * 256 + n_scales(N, K, group);
   const unsigned blocks = (unsigned)std::min<int64_t>((all + 255) / 256, 65536);
   hipLaunchKernelGGL(k_w4_pack, dim3(blocks), dim3(256), 0, s, N, K, (int64_t)group, q,
                      reinterpret_cast<const uint16_t*>(scale), zero, reinterpret_cast<uint32_t*>(packed),
@@ -292,8 +345,9 @@ hipError_t launch_w4_gemm(bool bf16, bool out_f32, bool zero, int64_t N, int64_t
   a.M = M;
   a.N = N;
   a.K = K;
+  a.bands = (int)n_bands(N);
   a.blocks = (int)n_blocks(K);
-  a.groups = (int)(K / group);
+  a.group = group;
   if (bf16) return out_f32 ? by_tokens<true, true>(a, s) : by_tokens<true, false>(a, s);
   return out_f32 ? by_tokens<false, true>(a, s) : by_tokens<false, false>(a, s);
 }

@@ -659,64 +659,63 @@ _APPEND_ARGS = struct.Struct("25q")
 _ATTENTION_ARGS = struct.Struct("7qd11q")
 _CACHE_ARGS = struct.Struct("8q")
 _LAYOUTS = {"half": 0, "interleaved": 1}
+_HALVES = {torch.float16: PATCH_F16, torch.bfloat16: PATCH_BF16}
 _SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "by_parts": 3}
 
 
-class _Device:
-    """Makes a tensor's device the current one for a call, where it is not:
-    a launch goes to the current device."""
-
-    def __init__(self, index: int):
-        self.index = index
-
-    def __enter__(self):
-        self.before = torch.cuda.current_device()
-        if self.before != self.index:
-            torch.cuda.set_device(self.index)
-
-    def __exit__(self, *exc):
-        if self.before != self.index:
-            torch.cuda.set_device(self.before)
+_get_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
 
 
-def _call(device: torch.device, fn, *args):
-    """A library call on the device's current stream."""
-    i = device.index
-    if torch.cuda.current_device() == i:
-        rc = fn(*args, _stream(i))
+def _call(index: int, fn, *args):
+    """A library call on the current stream of device `index`, which is made
+    the current device for it: a launch goes to the current device."""
+    if index == _get_device():
+        rc = fn(*args, _stream(index))
     else:
-        with _Device(i):
-            rc = fn(*args, _stream(i))
-    if rc != 0:
+        with torch.cuda.device(index):
+            rc = fn(*args, _stream(index))
+    if rc:
         _check(rc)
 
 
-def _heads(t, name: str, dtype, shape):
-    """A [tokens, heads, dim] tensor whose elements of a head are contiguous;
-    returns its address and the other two strides.  A size of None is free."""
-    _need(isinstance(t, torch.Tensor), f"{name} must be a torch tensor")
-    _need(t.dtype == dtype, f"{name} must be {dtype}, not {t.dtype}")
-    _need(t.dim() == 3, f"{name} must have three dimensions (tokens, heads, dim), not {t.dim()}")
+# The checks below build their messages only where they fail: a decode step's
+# calls last a few microseconds each.
+def _heads(t, name: str, dtype, T, H, D, index):
+    """A [tokens, heads, dim] tensor on device `index` whose elements of a
+    head are contiguous: its address, other strides, and heads (H None: any)."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} must be a torch tensor")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
     s = t.shape
-    _need(s[0] == shape[0] and (shape[1] is None or s[1] == shape[1]) and (shape[2] is None or s[2] == shape[2]),
-          f"{name} must have shape {tuple(shape)}, not {tuple(s)}")
+    if len(s) != 3 or s[0] != T or s[2] != D or (H is not None and s[1] != H):
+        raise ValueError(f"{name} must have shape {(T, 'heads' if H is None else H, D)}, not {tuple(s)}")
     st = t.stride()
-    _need(st[2] == 1 or s[2] == 1, f"{name}: the elements of a head must be contiguous")
-    return t.data_ptr(), st[0], st[1]
+    if st[2] != 1 and D > 1:
+        raise ValueError(f"{name}: the elements of a head must be contiguous")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on device {index}, not {t.device}")
+    return t.data_ptr(), st[0], st[1], s[1]
 
 
-def _index(t, name: str, n: int):
-    _need(isinstance(t, torch.Tensor), f"{name} must be a torch tensor")
-    _need(t.dtype == torch.int32 and t.dim() == 1 and t.shape[0] == n and (n < 2 or t.stride(0) == 1),
-          f"{name} must be a contiguous int32 tensor of {n}")
+def _index(t, name: str, n: int, index):
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or t.dim() != 1 or t.shape[0] != n or (
+            n > 1 and not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous int32 tensor of {n}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on device {index}, not {t.device}")
     return t.data_ptr()
 
 
-def _on_device(device, *named):
-    _need(device.type == "cuda", "tensors must be on the device")
-    for name, t in named:
-        if t is not None:
-            _need(t.device == device, f"{name} must be on {device}, not {t.device}")
+def _device_of(t, name: str) -> int:
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} must be a torch tensor")
+    return t.get_device()
+
+
+def _need_device(index: int):
+    if index < 0:
+        raise ValueError("tensors must be on the device")
 
 
 def rope_table(positions: int, rot: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
@@ -731,18 +730,22 @@ def rope_table(positions: int, rot: int, base: float = 10000.0, scaling: str = "
     if out is None:
         _need(positions >= 1 and rot >= 2, f"positions={positions} and rot={rot} must be positive")
         out = torch.empty((positions, rot), dtype=torch.float32, device=device)
-    _on_device(out.device)
-    _call(out.device, lib.patch_rope_table, positions, rot, base, _SCALINGS[scaling], factor, original, low, high,
+    _need_device(out.get_device())
+    _call(out.get_device(), lib.patch_rope_table, positions, rot, base, _SCALINGS[scaling], factor, original, low, high,
           magnitude, out.data_ptr())
     return out
 
 
-def _table_of(table: Optional[torch.Tensor]):
+def _table_of(table: Optional[torch.Tensor], index):
     if table is None:
         return 0, 0, 0
-    _need(isinstance(table, torch.Tensor) and table.dtype == torch.float32 and table.dim() == 2
-          and table.is_contiguous(), "table must be a contiguous float32 tensor (positions, rot)")
-    return table.data_ptr(), table.shape[0], table.shape[1]
+    if not isinstance(table, torch.Tensor) or table.dtype is not torch.float32 or table.dim() != 2 or \
+            not table.is_contiguous():
+        raise ValueError("table must be a contiguous float32 tensor (positions, rot)")
+    if table.get_device() != index:
+        raise ValueError(f"table must be on device {index}, not {table.device}")
+    n, rot = table.shape
+    return table.data_ptr(), n, rot
 
 
 def rope(x: torch.Tensor, positions: torch.Tensor, table: torch.Tensor, layout: str = "half", inverse: bool = False,
@@ -752,21 +755,23 @@ def rope(x: torch.Tensor, positions: torch.Tensor, table: torch.Tensor, layout: 
     (patch_rope).  inverse=True turns back: the gradient of x from that of
     the result.  out may be x."""
     lib = _lib or load()
-    _need(layout in _LAYOUTS, f"layout must be one of {sorted(_LAYOUTS)}, not {layout!r}")
-    _need(isinstance(x, torch.Tensor) and x.dim() == 3, "x must be a 3-D tensor (tokens, heads, dim)")
-    _need(x.dtype in _TORCH_DT, f"unsupported dtype {x.dtype}")
+    if layout not in _LAYOUTS:
+        raise ValueError(f"layout must be one of {sorted(_LAYOUTS)}, not {layout!r}")
+    if not isinstance(x, torch.Tensor) or x.dim() != 3:
+        raise ValueError("x must be a 3-D tensor (tokens, heads, dim)")
+    dt, dtype, index = x.dtype, _dt(x.dtype), x.get_device()
     T, H, D = x.shape
-    xp, xt, xh = _heads(x, "x", x.dtype, (T, H, D))
-    pos = _index(positions, "positions", T)
-    _need(table is not None, "table must be a tensor")
-    tp, context, rot = _table_of(table)
-    _on_device(x.device, ("positions", positions), ("table", table), ("out", out))
+    xp, xt, xh, _ = _heads(x, "x", dt, T, H, D, index)
+    pos = _index(positions, "positions", T, index)
+    tp, context, rot = _table_of(table, index)
+    if not rot:
+        raise ValueError("table must be a tensor with rot > 0 columns")
+    _need_device(index)
     if out is None:
-        out = torch.empty((T, H, D), dtype=x.dtype, device=x.device)
-    op, ot, oh = _heads(out, "out", x.dtype, (T, H, D))
-    _call(x.device, lib.patch_rope,
-          _ROPE_ARGS.pack(_TORCH_DT[x.dtype], _LAYOUTS[layout], bool(inverse), T, H, D, rot, context, xp, xt, xh, op, ot,
-                          oh, pos, tp))
+        out = torch.empty((T, H, D), dtype=dt, device=x.device)
+    op, ot, oh, _ = _heads(out, "out", dt, T, H, D, index)
+    _call(index, lib.patch_rope,
+          _ROPE_ARGS.pack(dtype, _LAYOUTS[layout], bool(inverse), T, H, D, rot, context, xp, xt, xh, op, ot, oh, pos, tp))
     return out
 
 
@@ -792,10 +797,13 @@ class KVCache:
         pages, heads, page, dim = k.shape
         _need(page in (16, 32, 64, 128), f"pages must hold 16, 32, 64 or 128 tokens, not {page}")
         _need(dim % 16 == 0 and 16 <= dim <= 256, f"dim must be a multiple of 16 up to 256, not {dim}")
-        _on_device(k.device, ("v", self.v), ("k_scale", self.k_scale), ("v_scale", self.v_scale))
+        _need_device(k.get_device())
+        for name in ("v", "k_scale", "v_scale"):
+            _need(getattr(self, name).device == k.device, f"{name} must be on {k.device}")
         object.__setattr__(self, "_args", _CACHE_ARGS.pack(
             k.data_ptr(), self.v.data_ptr(), self.k_scale.data_ptr(), self.v_scale.data_ptr(), pages, heads, page, dim))
         object.__setattr__(self, "_shape", (pages, heads, page, dim))
+        object.__setattr__(self, "_index", k.get_device())
 
 
 def kv_cache(pages: int, kv_heads: int, dim: int, page: int = 64, device="cuda") -> KVCache:
@@ -806,12 +814,24 @@ def kv_cache(pages: int, kv_heads: int, dim: int, page: int = 64, device="cuda")
     return KVCache(kv[0], kv[1], scales[0], scales[1])
 
 
-def _pages_of(page_table: torch.Tensor):
-    _need(isinstance(page_table, torch.Tensor) and page_table.dtype == torch.int32 and page_table.dim() == 2
-          and (page_table.stride(1) == 1 or page_table.shape[1] < 2),
-          "page_table must be an int32 tensor (sequences, pages), each row contiguous")
+def _pages_of(page_table: torch.Tensor, index):
+    if not isinstance(page_table, torch.Tensor) or page_table.dtype is not torch.int32 or page_table.dim() != 2:
+        raise ValueError("page_table must be an int32 tensor (sequences, pages)")
     S, n = page_table.shape
-    return page_table.data_ptr(), S, n, max(page_table.stride(0), n)
+    st = page_table.stride()
+    if st[1] != 1 and n > 1:
+        raise ValueError("page_table: each row must be contiguous")
+    if page_table.get_device() != index:
+        raise ValueError(f"page_table must be on device {index}, not {page_table.device}")
+    return page_table.data_ptr(), S, n, st[0] if S > 1 else n
+
+
+def _cache_of(cache, index):
+    if not isinstance(cache, KVCache):
+        raise ValueError("cache must be a KVCache")
+    if cache._index != index:
+        raise ValueError(f"cache must be on device {index}, not {cache.k.device}")
+    return cache._shape
 
 
 def kv_append(k: torch.Tensor, v: torch.Tensor, cache: KVCache, page_table: torch.Tensor, kv_lens: torch.Tensor,
@@ -825,31 +845,30 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, cache: KVCache, page_table: torc
     rope_table, or None for no rotation.  Returns the rotated q (q_out,
     which may be q), or None."""
     lib = _lib or load()
-    _need(isinstance(cache, KVCache), "cache must be a KVCache")
-    _need(layout in _LAYOUTS, f"layout must be one of {sorted(_LAYOUTS)}, not {layout!r}")
-    _need(isinstance(k, torch.Tensor) and k.dim() == 3, "k must be a 3-D tensor (tokens, kv_heads, dim)")
-    _need(k.dtype in (torch.float16, torch.bfloat16), "k must be float16 or bfloat16")
-    _, hk, _, D = cache._shape
+    if layout not in _LAYOUTS:
+        raise ValueError(f"layout must be one of {sorted(_LAYOUTS)}, not {layout!r}")
+    index = _device_of(k, "k")
+    _, hk, _, D = _cache_of(cache, index)
+    dt = k.dtype
+    if dt not in _HALVES or k.dim() != 3:
+        raise ValueError("k must be a float16 or bfloat16 3-D tensor (tokens, kv_heads, dim)")
     T = k.shape[0]
-    kp, kt, kh = _heads(k, "k", k.dtype, (T, hk, D))
-    vp, vt, vh = _heads(v, "v", k.dtype, (T, hk, D))
-    pp, S, max_pages, row = _pages_of(page_table)
-    lens, cu = _index(kv_lens, "kv_lens", S), _index(cu_new, "cu_new", S + 1)
-    tp, context, rot = _table_of(table)
-    _on_device(k.device, ("cache", cache.k), ("v", v), ("q", q), ("q_out", q_out), ("page_table", page_table),
-               ("kv_lens", kv_lens), ("cu_new", cu_new), ("table", table))
+    kp, kt, kh, _ = _heads(k, "k", dt, T, hk, D, index)
+    vp, vt, vh, _ = _heads(v, "v", dt, T, hk, D, index)
+    pp, S, max_pages, row = _pages_of(page_table, index)
+    lens, cu = _index(kv_lens, "kv_lens", S, index), _index(cu_new, "cu_new", S + 1, index)
+    tp, context, rot = _table_of(table, index)
     qp = qt = qh = op = ot = oh = heads = 0
     if q is not None:
-        qp, qt, qh = _heads(q, "q", k.dtype, (T, None, D))
-        heads = q.shape[1]
+        qp, qt, qh, heads = _heads(q, "q", dt, T, None, D, index)
         if q_out is None:
-            q_out = torch.empty((T, heads, D), dtype=k.dtype, device=k.device)
-        op, ot, oh = _heads(q_out, "q_out", k.dtype, (T, heads, D))
-    else:
-        _need(q_out is None, "q_out without q")
-    _call(k.device, lib.patch_kv_append,
-          _APPEND_ARGS.pack(_TORCH_DT[k.dtype], _LAYOUTS[layout], T, S, heads, rot, context, max_pages, kp, kt, kh, vp, vt,
-                            vh, qp, qt, qh, op, ot, oh, pp, row, lens, cu, tp), cache._args)
+            q_out = torch.empty((T, heads, D), dtype=dt, device=k.device)
+        op, ot, oh, _ = _heads(q_out, "q_out", dt, T, heads, D, index)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    _call(index, lib.patch_kv_append,
+          _APPEND_ARGS.pack(_HALVES[dt], _LAYOUTS[layout], T, S, heads, rot, context, max_pages, kp, kt, kh, vp, vt, vh, qp,
+                            qt, qh, op, ot, oh, pp, row, lens, cu, tp), cache._args)
     return q_out
 
 
@@ -869,34 +888,36 @@ def attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, kv_lens
     float32 [tokens, heads] to take the logarithm of each softmax's sum.
     workspace as for gemm."""
     lib = _lib or load()
-    _need(isinstance(cache, KVCache), "cache must be a KVCache")
-    _need(isinstance(q, torch.Tensor) and q.dim() == 3, "q must be a 3-D tensor (tokens, heads, dim)")
-    _need(q.dtype in (torch.float16, torch.bfloat16), "q must be float16 or bfloat16")
-    _, hk, _, D = cache._shape
+    index = _device_of(q, "q")
+    _, hk, _, D = _cache_of(cache, index)
+    dt = q.dtype
+    if dt not in _HALVES or q.dim() != 3:
+        raise ValueError("q must be a float16 or bfloat16 3-D tensor (tokens, heads, dim)")
     T, H, _ = q.shape
-    qp, qt, qh = _heads(q, "q", q.dtype, (T, H, D))
-    pp, S, max_pages, row = _pages_of(page_table)
-    lens, cu = _index(kv_lens, "kv_lens", S), _index(cu_new, "cu_new", S + 1)
-    od = out_dtype or q.dtype
-    _check_out_dtype(od, q.dtype)
-    _on_device(q.device, ("cache", cache.k), ("page_table", page_table), ("kv_lens", kv_lens), ("cu_new", cu_new),
-               ("out", out), ("lse", lse))
+    qp, qt, qh, _ = _heads(q, "q", dt, T, H, D, index)
+    pp, S, max_pages, row = _pages_of(page_table, index)
+    lens, cu = _index(kv_lens, "kv_lens", S, index), _index(cu_new, "cu_new", S + 1, index)
+    od = out_dtype or dt
+    if od is not dt:
+        _check_out_dtype(od, dt)
     if out is None:
         out = torch.empty((T, H, D), dtype=od, device=q.device)
-    op, ot, oh = _heads(out, "out", od, (T, H, D))
+    op, ot, oh, _ = _heads(out, "out", od, T, H, D, index)
+    lp = 0
     if lse is not None:
         _check_dev(lse, "lse", torch.float32, (T, H))
-    ws, nb = None, 0
+        _need(lse.get_device() == index, f"lse must be on device {index}")
+        lp = lse.data_ptr()
+    wp, nb = None, 0
     if workspace is not None:
-        nb = _ws_bytes("attention", (T, S), (H, hk), D, q.device.index,
-                       lambda: lib.patch_attention_workspace_bytes(T, S, H, hk, D))
+        nb = _ws_bytes("attention", (T, S), (H, hk), D, index, lambda: lib.patch_attention_workspace_bytes(T, S, H, hk, D))
         ws = _workspace(nb, workspace, q.device)
-        nb = 0 if ws is None else ws.numel() * ws.element_size()
-    _call(q.device, lib.patch_attention,
-          _ATTENTION_ARGS.pack(_TORCH_DT[q.dtype], _TORCH_DT[od], T, S, H, max_pages, window,
-                               D ** -0.5 if scale is None else scale, qp, qt, qh, op, ot, oh,
-                               0 if lse is None else lse.data_ptr(), pp, row, lens, cu),
-          cache._args, None if ws is None else ws.data_ptr(), nb)
+        if ws is not None:
+            wp, nb = ws.data_ptr(), ws.numel() * ws.element_size()
+    _call(index, lib.patch_attention,
+          _ATTENTION_ARGS.pack(_HALVES[dt], _TORCH_DT[od], T, S, H, max_pages, window, D ** -0.5 if scale is None else scale,
+                               qp, qt, qh, op, ot, oh, lp, pp, row, lens, cu),
+          cache._args, wp, nb)
     return out
 
 
@@ -922,11 +943,11 @@ def w4_quantize(W: torch.Tensor, group: int = 128, zero: bool = False):
     _check_dev(W, "W", on_device=False)
     N, K = W.shape
     _need(group in (32, 64, 128) and K % group == 0 and N > 0 and K > 0, f"K={K} must be a multiple of the group ({group}: 32, 64 or 128)")
-    _on_device(W.device)
+    _need_device(W.get_device())
     q = torch.empty((N, K // 2), dtype=torch.uint8, device=W.device)
     scale = torch.empty((N, K // group), dtype=W.dtype, device=W.device)
     z = torch.empty((N, K // group), dtype=torch.uint8, device=W.device) if zero else None
-    _call(W.device, lib.patch_w4_quantize, _TORCH_DT[W.dtype], N, K, group, W.data_ptr(), q.data_ptr(), scale.data_ptr(),
+    _call(W.get_device(), lib.patch_w4_quantize, _HALVES[W.dtype], N, K, group, W.data_ptr(), q.data_ptr(), scale.data_ptr(),
           None if z is None else z.data_ptr())
     return q, scale, z
 
@@ -944,9 +965,10 @@ def w4_pack(q: torch.Tensor, scale: torch.Tensor, zero: Optional[torch.Tensor], 
     _need(scale.dtype in (torch.float16, torch.bfloat16), "scale must be float16 or bfloat16")
     if zero is not None:
         _check_dev(zero, "zero", torch.uint8, (N, K // group), on_device=False)
-    _on_device(q.device, ("scale", scale), ("zero", zero))
+    _need_device(q.get_device())
+    _need(scale.device == q.device and (zero is None or zero.device == q.device), "scale and zero must be on q's device")
     packed = torch.empty(int(lib.patch_w4_bytes(N, K, group, zero is not None)), dtype=torch.uint8, device=q.device)
-    _call(q.device, lib.patch_w4_pack, _TORCH_DT[scale.dtype], N, K, group, q.data_ptr(), scale.data_ptr(),
+    _call(q.get_device(), lib.patch_w4_pack, _HALVES[scale.dtype], N, K, group, q.data_ptr(), scale.data_ptr(),
           None if zero is None else zero.data_ptr(), packed.data_ptr(), packed.numel())
     return W4Weight(packed, scale.dtype, N, K, group, zero is not None)
 
@@ -955,15 +977,24 @@ def w4_gemm(X: torch.Tensor, weight: W4Weight, out_dtype: Optional[torch.dtype] 
             out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Y = X W^T with 4-bit weights (patch_w4_gemm)."""
     lib = _lib or load()
-    _need(isinstance(weight, W4Weight), "weight must be a W4Weight (w4_pack)")
-    _check_x(X, weight.dtype, weight.K)
+    if not isinstance(weight, W4Weight):
+        raise ValueError("weight must be a W4Weight (w4_pack)")
+    dt, N, K, index = weight.dtype, weight.N, weight.K, _device_of(X, "X")
+    if X.dtype is not dt or X.dim() != 2 or X.shape[1] != K or not X.is_contiguous():
+        raise ValueError(f"X must be a contiguous {dt} tensor (M, {K}), not {X.dtype} {tuple(X.shape)}")
     M = X.shape[0]
-    od = out_dtype or X.dtype
-    _check_out_dtype(od, X.dtype)
-    _check_out(out, (M, weight.N), od)
-    _on_device(X.device, ("weight", weight.packed), ("out", out))
+    od = out_dtype or dt
+    if od is not dt:
+        _check_out_dtype(od, dt)
+    packed = weight.packed
+    if packed.get_device() != index:
+        raise ValueError(f"weight must be on device {index}, not {packed.device}")
+    _need_device(index)
     if out is None:
-        out = torch.empty((M, weight.N), dtype=od, device=X.device)
-    _call(X.device, lib.patch_w4_gemm, _TORCH_DT[weight.dtype], weight.N, weight.K, weight.group, weight.with_zero,
-          weight.packed.data_ptr(), weight.packed.numel(), X.data_ptr(), M, out.data_ptr(), _TORCH_DT[od])
+        out = torch.empty((M, N), dtype=od, device=X.device)
+    else:
+        _check_out(out, (M, N), od)
+        _need(out.get_device() == index, f"out must be on device {index}")
+    _call(index, lib.patch_w4_gemm, _HALVES[dt], N, K, weight.group, weight.with_zero, packed.data_ptr(), packed.numel(),
+          X.data_ptr(), M, out.data_ptr(), _TORCH_DT[od])
     return out

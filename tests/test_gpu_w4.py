@@ -55,13 +55,15 @@ def test_packed_bytes_are_as_stated():
                         k = block * 128 + 32 * j + 8 * (l // 16) + 2 * i
                         row = band * 16 + l % 16
                         assert (word >> (4 * i)) & 15 == int(val[row, k]) and (word >> (16 + 4 * i)) & 15 == int(val[row, k + 1])
-    s = torch.zeros(32, 5, dtype=torch.float16)
-    s[:N] = scale.cpu()
+    # band, block, quad of rows, group, row of the quad
+    s = torch.zeros(32, 8, dtype=torch.float16)
+    s[:N, :5] = scale.cpu()
+    order = lambda t: t.view(2, 4, 4, 2, 4).permute(0, 3, 1, 4, 2)  # noqa: E731
     at = 4096
-    assert torch.equal(p[at:at + 2 * 5 * 16 * 2].view(torch.float16).view(2, 5, 16), s.view(2, 16, 5).transpose(1, 2))
-    zz = torch.zeros(32, 5, dtype=torch.uint8)
-    zz[:N] = z.cpu()
-    assert torch.equal(p[at + 320:].view(2, 5, 16), zz.view(2, 16, 5).transpose(1, 2))
+    assert torch.equal(p[at:at + 32 * 8 * 2].view(torch.float16).view(2, 2, 4, 4, 4), order(s))
+    zz = torch.zeros(32, 8, dtype=torch.uint8)
+    zz[:N, :5] = z.cpu()
+    assert torch.equal(p[at + 512:].view(2, 2, 4, 4, 4), order(zz))
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])

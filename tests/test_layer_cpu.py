@@ -134,8 +134,8 @@ def test_w4_shapes_refused(N, K, group, status):
 def test_w4_arguments_refused():
     lib = patch.load()
     n = lib.patch_w4_bytes(40, 160, 32, 1)
-    # 3 bands of 2 blocks of 1 KB, 3 x 16 rows of 5 groups of a 2-byte scale and a zero byte
-    assert n == 3 * 2 * 1024 + 48 * 5 * 3
+    # 3 bands of 2 blocks of 1 KB, 3 x 16 rows of 8 groups (K padded to 256) of a 2-byte scale and a zero byte
+    assert n == 3 * 2 * 1024 + 48 * 8 * 3
     g = lambda dt=1, z=1, p=P, b=n, x=P, m=1, y=P, yd=1: _name(  # noqa: E731
         lib.patch_w4_gemm(dt, 40, 160, 32, z, V(p), b, V(x), m, V(y), yd, None))
     assert g(dt=2) == g(yd=0) == g(m=-1) == g(p=0) == g(x=0) == g(y=0) == g(p=P + 8) == g(x=P + 2) == "PATCH_ERR_INVALID_ARG"
