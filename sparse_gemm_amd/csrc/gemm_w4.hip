@@ -16,7 +16,7 @@
 //     cancellation costs three bits of an fp32 sum at most.
 //   * A band's weights lie in lane order (patch_w4_pack), 1 KB for 128 columns:
 //     one 16-byte load a lane feeds four matrix instructions.
-//   * A workgroup has one or two bands of 16 rows; its waves take the 128-column
+//   * A workgroup has one to four bands of 16 rows; its waves take the 128-column
 //     blocks in turn, the next block's bytes on their way while one is used, and
 //     join their sums through LDS in a fixed order.
 #include <algorithm>
@@ -27,19 +27,7 @@
 namespace patch {
 namespace {
 
-#ifndef WB
-#define WB 2
-#endif
-#ifndef KWV
-#define KWV 8
-#endif
-constexpr int kMaxWaves = KWV;
-#ifndef RBMIN
-#define RBMIN 512
-#endif
-#ifndef RBX
-#define RBX 2
-#endif
+constexpr int kMaxWaves = 8;
 
 // The eight operand elements 16 + q of a packed word.
 template <bool BF16>
@@ -279,7 +267,7 @@ hipError_t go(const W4Args& a, hipStream_t s) {
   const int64_t my = (a.M + 16 * MT - 1) / (16 * MT);
   if (my > 65535) return hipErrorInvalidValue;
   // a wave takes two blocks or more where there are enough
-  const int waves = std::max(1, std::min(kMaxWaves, a.blocks / WB));
+  const int waves = std::max(1, std::min(kMaxWaves, a.blocks / 2));
   const size_t lds = (size_t)waves * RB * MT * 1024;
   hipLaunchKernelGGL((k_w4<BF16, OUT_F32, MT, RB, G, ZERO>), dim3((unsigned)((a.bands + RB - 1) / RB), (unsigned)my),
                      dim3(64 * waves), lds, s, a);
@@ -299,9 +287,19 @@ hipError_t by_group(const W4Args& a, hipStream_t s) {
 }
 template <bool BF16, bool OUT_F32>
 hipError_t by_tokens(const W4Args& a, hipStream_t s) {
-  // more than four tokens: X is most of what a wave reads, and two bands share it
-  if (a.M <= 16) return a.M > 4 && a.bands >= RBMIN ? by_group<BF16, OUT_F32, 1, RBX>(a, s) : by_group<BF16, OUT_F32, 1, 1>(a, s);
-  return by_group<BF16, OUT_F32, 2, 1>(a, s);
+  // A workgroup of three or four bands has a CU to itself, and what does not fit
+  // in one round waits for a second: as many bands as make one round.  11008 x
+  // 4096 (688 bands), 16 tokens: 16.1 us with two bands, 11.5 with three, 12.9
+  // with four.
+  const int round = (a.bands + cu_count() - 1) / cu_count();
+  if (a.M > 16) return round <= 1 ? by_group<BF16, OUT_F32, 2, 1>(a, s) : by_group<BF16, OUT_F32, 2, 2>(a, s);
+  switch (round) {
+    case 0:
+    case 1: return by_group<BF16, OUT_F32, 1, 1>(a, s);
+    case 2: return by_group<BF16, OUT_F32, 1, 2>(a, s);
+    case 3: return by_group<BF16, OUT_F32, 1, 3>(a, s);
+    default: return by_group<BF16, OUT_F32, 1, 4>(a, s);
+  }
 }
 
 }  // namespace
