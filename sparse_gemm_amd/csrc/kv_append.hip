@@ -53,20 +53,15 @@ __device__ __forceinline__ float nan_unless_finite(float x) {
 // Store an item's values, scaled and rounded, into a cache row.
 template <int V>
 __device__ __forceinline__ void store_item_e4m3(uint8_t* row, const ItemPlace& p, const Item<V>& r, float inv) {
-  float x[2 * V];
+  float x[V], y[V];
+  runs_of(p, r, x, y);
 #pragma unroll
   for (int i = 0; i < V; i++) {
-    const float a = nan_unless_finite(r.a[i] * inv), b = nan_unless_finite(r.b[i] * inv);
-    if (p.interleaved) {
-      x[2 * i] = a;
-      x[2 * i + 1] = b;
-    } else {
-      x[i] = a;
-      x[V + i] = b;
-    }
+    x[i] = nan_unless_finite(x[i] * inv);
+    y[i] = nan_unless_finite(y[i] * inv);
   }
   if constexpr (V == 1) {
-    const uint32_t w = to_e4m3x4(x[0], x[1], 0.f, 0.f);
+    const uint32_t w = to_e4m3x4(x[0], y[0], 0.f, 0.f);
     row[p.first] = (uint8_t)w;
     row[p.second] = (uint8_t)(w >> 8);
   } else {
@@ -74,7 +69,7 @@ __device__ __forceinline__ void store_item_e4m3(uint8_t* row, const ItemPlace& p
 #pragma unroll
     for (int i = 0; i < V / 4; i++) {
       u.v[i] = to_e4m3x4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-      w.v[i] = to_e4m3x4(x[V + 4 * i], x[V + 4 * i + 1], x[V + 4 * i + 2], x[V + 4 * i + 3]);
+      w.v[i] = to_e4m3x4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
     }
     *reinterpret_cast<Vec<uint32_t, V / 4>*>(row + p.first) = u;
     *reinterpret_cast<Vec<uint32_t, V / 4>*>(row + p.second) = w;
@@ -96,31 +91,35 @@ __device__ __forceinline__ float group_max(float x, float* lds) {
 
 // GW lanes a block, KEEP items of a lane held in registers.
 template <typename T, int V, int GW, int KEEP>
-__global__ __launch_bounds__(kThreads) void k_kv_append(patch_kv_append_args a, patch_kv_cache c, uint32_t kv_blocks) {
+__global__ __launch_bounds__(kThreads) void k_kv_append(patch_kv_append_args a, patch_kv_cache c, uint32_t kv_blocks,
+                                                        int q_tokens) {
   __shared__ float lds[kThreads / 64];
   const int rot = (int)a.rot, D = (int)c.dim, items = D / (2 * V), B = (int)c.page;
   const bool inter = a.layout == PATCH_ROPE_INTERLEAVED;
   const int S = (int)a.S;
   const int32_t* cu = a.cu_new_dev;
 
-  if (blockIdx.x >= kv_blocks) {  // one token's q
-    const int t = (int)(blockIdx.x - kv_blocks);
-    const int s = find_last(S, [&](int i) { return cu[i] <= t; });
-    if (t < cu[s] || t >= cu[s + 1]) return;
-    const int64_t pos = (int64_t)a.kv_lens_dev[s] - (cu[s + 1] - t);
-    const float* row = a.table_dev && pos >= 0 && pos < a.context ? a.table_dev + pos * rot : nullptr;
-    const T* x = reinterpret_cast<const T*>(a.q_dev) + (int64_t)t * a.q_token;
-    T* o = reinterpret_cast<T*>(a.q_out_dev) + (int64_t)t * a.q_out_token;
+  if (blockIdx.x >= kv_blocks) {  // q of q_tokens tokens
+    const int ta = (int)(blockIdx.x - kv_blocks) * q_tokens, tb = min(ta + q_tokens, (int)a.T);
+    int s = find_last(S, [&](int i) { return cu[i] <= ta; });
     const int per = kThreads / items;  // heads at a time (items <= 128)
     const int ci = (int)threadIdx.x % items;
     if ((int)threadIdx.x >= per * items) return;
-    ItemPlace p = item_place<V>(ci, a.table_dev ? rot : 0, inter);
-    Angles<V> g;
-    if (p.turned) g = load_angles<V>(row, ci, rot, false);
-    for (int h = (int)threadIdx.x / items; h < (int)a.heads; h += per) {
-      Item<V> r = load_item<T, V>(x + h * a.q_head, p);
-      if (p.turned) turn(r, g);
-      store_item<T, V>(o + h * a.q_out_head, p, r);
+    const ItemPlace p = item_place<V>(ci, a.table_dev ? rot : 0, D, inter);
+    for (int t = ta; t < tb; t++) {
+      while (s + 1 < S && t >= cu[s + 1]) s++;
+      if (t < cu[s] || t >= cu[s + 1]) continue;
+      const int64_t pos = (int64_t)a.kv_lens_dev[s] - (cu[s + 1] - t);
+      const float* row = a.table_dev && pos >= 0 && pos < a.context ? a.table_dev + pos * rot : nullptr;
+      const T* x = reinterpret_cast<const T*>(a.q_dev) + (int64_t)t * a.q_token;
+      T* o = reinterpret_cast<T*>(a.q_out_dev) + (int64_t)t * a.q_out_token;
+      Angles<V> g;
+      if (p.turned) g = load_angles<V>(row, p, rot, false);
+      for (int h = (int)threadIdx.x / items; h < (int)a.heads; h += per) {
+        Item<V> r = load_item<T, V>(x + h * a.q_head, p);
+        if (p.turned) turn(r, g);
+        store_item<T, V>(o + h * a.q_out_head, p, r);
+      }
     }
     return;
   }
@@ -167,11 +166,11 @@ __global__ __launch_bounds__(kThreads) void k_kv_append(patch_kv_append_args a, 
 
   auto get = [&](int e, ItemPlace& p) {
     const int r = e / items, ci = e - r * items;
-    p = item_place<V>(ci, rotates ? rot : 0, inter);
+    p = item_place<V>(ci, rotates ? rot : 0, D, inter);
     Item<V> x = load_item<T, V>(src + (t0 + r) * stride, p);
     if (p.turned) {
       const int64_t pos = lo + r;
-      turn(x, load_angles<V>(pos < a.context ? a.table_dev + pos * rot : nullptr, ci, rot, false));
+      turn(x, load_angles<V>(pos < a.context ? a.table_dev + pos * rot : nullptr, p, rot, false));
     }
     return x;
   };
@@ -218,7 +217,7 @@ __global__ __launch_bounds__(kThreads) void k_kv_append(patch_kv_append_args a, 
     const int e = k * GW + lane;
     if (e < total) {
       const int r = e / items;
-      store_item_e4m3<V>(cache + (first_slot + r) * D, item_place<V>(e - r * items, rotates ? rot : 0, inter), kept[k],
+      store_item_e4m3<V>(cache + (first_slot + r) * D, item_place<V>(e - r * items, rotates ? rot : 0, D, inter), kept[k],
                          inv);
     }
   }
@@ -242,17 +241,28 @@ hipError_t go(const patch_kv_append_args& a, const patch_kv_cache& c, hipStream_
     constexpr int groups = 64 / (GW < 64 ? GW : 64);
     blocks = (units * ((kinds + groups - 1) / groups) + kThreads / 64 - 1) / (kThreads / 64);
   }
-  const int64_t all = blocks + (a.q_dev ? a.T : 0);
+  // a workgroup rotates the q of two tokens where that leaves 8 a CU
+  const int q_tokens = a.T >= 2 * 2048 ? 2 : 1;
+  const int64_t all = blocks + (a.q_dev ? (a.T + q_tokens - 1) / q_tokens : 0);
   if (all > 0x7fffffff) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((k_kv_append<T, V, GW, KEEP>), dim3((unsigned)all), dim3(kThreads), 0, s, a, c, (uint32_t)blocks);
+  hipLaunchKernelGGL((k_kv_append<T, V, GW, KEEP>), dim3((unsigned)all), dim3(kThreads), 0, s, a, c, (uint32_t)blocks,
+                     q_tokens);
   return hipGetLastError();
 }
 
 // A sequence brings up to two tokens on average: 8 lanes a block.  More: a
-// workgroup a block.
+// workgroup a block, which keeps the whole block in registers, 2V values an item.
 template <typename T, int V>
 hipError_t by_tokens(const patch_kv_append_args& a, const patch_kv_cache& c, hipStream_t s) {
-  return a.T <= 2 * a.S ? go<T, V, 8, 1>(a, c, s) : go<T, V, 256, V == 8 ? 4 : V == 4 ? 8 : 1>(a, c, s);
+  if (a.T <= 2 * a.S) return go<T, V, 8, 1>(a, c, s);
+  if constexpr (V == 1) {
+    return go<T, 1, 256, 4>(a, c, s);
+  } else {
+    const int64_t values = c.page * c.dim / kThreads;  // of a thread
+    return values <= 16   ? go<T, V, 256, 8 / V>(a, c, s)
+           : values <= 32 ? go<T, V, 256, 16 / V>(a, c, s)
+                          : go<T, V, 256, 32 / V>(a, c, s);
+  }
 }
 
 template <typename T>

@@ -45,13 +45,13 @@ __global__ __launch_bounds__(kThreads) void k_rope(patch_rope_args a, uint32_t t
   if (e >= threads) return;
   const uint32_t t = e / items, c = e - t * items;
   const int rot = (int)a.rot;
-  const ItemPlace p = item_place<V>((int)c, rot, a.layout == PATCH_ROPE_INTERLEAVED);
+  const ItemPlace p = item_place<V>((int)c, rot, (int)a.D, a.layout == PATCH_ROPE_INTERLEAVED);
   const T* x = reinterpret_cast<const T*>(a.x_dev) + (int64_t)t * a.x_token;
   T* o = reinterpret_cast<T*>(a.out_dev) + (int64_t)t * a.out_token;
   Angles<V> g;
   if (p.turned) {
     const int pos = a.positions_dev[t];
-    g = load_angles<V>(pos >= 0 && pos < a.context ? a.table_dev + (int64_t)pos * rot : nullptr, (int)c, rot,
+    g = load_angles<V>(pos >= 0 && pos < a.context ? a.table_dev + (int64_t)pos * rot : nullptr, p, rot,
                        a.inverse != 0);
   } else if (a.x_dev == a.out_dev) {
     return;  // in place: the elements behind rot are there already

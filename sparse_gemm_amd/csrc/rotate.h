@@ -2,12 +2,13 @@
 // kernel and the cache append.
 //
 // A head of D elements is cut into D / 2V items of 2V elements, one item a
-// thread: an item c < rot / 2V is V pairs (HALF: elements cV.. and rot/2 +
-// cV..; INTERLEAVED: 2cV .. 2cV + 2V - 1), a later one 2V elements that pass
-// unchanged.  Either way pair i of the head takes entry i of the table row's
-// cos half and of its sin half, so an item reads V consecutive floats of each.
-// V is 8 where the sizes and addresses allow 16-byte accesses of 16-bit
-// elements, else 4, else 1 (choose_v).
+// thread, in two runs of V: the c-th run of the first half and of the second
+// half of the rotated elements, or of those behind them, which pass unchanged.
+// So neighbouring threads read neighbouring runs, in either layout.  HALF:
+// the runs are the two elements of V pairs; INTERLEAVED: each holds V / 2
+// pairs (V = 1: the runs are neighbours, one pair).  V is 8 where sizes and
+// addresses allow 16-byte accesses of 16-bit elements, else 4, else 1
+// (choose_v).
 #pragma once
 
 #include "layer_common.h"
@@ -16,26 +17,33 @@ namespace patch {
 
 template <int V>
 struct Item {
-  float a[V], b[V];  // first and second element of each pair (rotated items), or elements 0.. and V.. (others)
+  float a[V], b[V];  // first and second element of each pair (rotated items), or the two runs (others)
 };
 
-// first element of an item's first and second run of V (pairs) elements
+// Where an item's runs begin, and its first pair and that of its second run's.
 struct ItemPlace {
-  int first, second;
+  int first, second, pair0, pair1;
   bool turned, interleaved;
 };
 
 template <int V>
-__device__ __forceinline__ ItemPlace item_place(int c, int rot, bool interleaved) {
+__device__ __forceinline__ ItemPlace item_place(int c, int rot, int D, bool interleaved) {
   ItemPlace p;
-  p.turned = c < rot / (2 * V);
+  const int turning = rot / (2 * V);
+  p.turned = c < turning;
   p.interleaved = interleaved && p.turned;
-  if (p.turned && !interleaved) {
-    p.first = c * V;
-    p.second = rot / 2 + c * V;
-  } else {
-    p.first = 2 * c * V;
-    p.second = p.first + V;
+  const int from = p.turned ? 0 : rot, size = p.turned ? rot : D - rot, i = p.turned ? c : c - turning;
+  p.first = from + i * V;
+  p.second = p.first + size / 2;
+  p.pair0 = p.pair1 = c * V;
+  if (p.interleaved) {
+    if constexpr (V == 1) {
+      p.first = 2 * c;
+      p.second = 2 * c + 1;
+    } else {
+      p.pair0 = p.first / 2;
+      p.pair1 = p.second / 2;
+    }
   }
   return p;
 }
@@ -45,12 +53,13 @@ __device__ __forceinline__ Item<V> load_item(const T* head, const ItemPlace& p) 
   const Vec<T, V> x = *reinterpret_cast<const Vec<T, V>*>(head + p.first);
   const Vec<T, V> y = *reinterpret_cast<const Vec<T, V>*>(head + p.second);
   Item<V> r;
-  if (p.interleaved) {
+  if (V > 1 && p.interleaved) {
 #pragma unroll
-    for (int i = 0; i < V; i++) {  // pair i = elements 2i, 2i + 1 of the 2V
-      const int e = 2 * i, o = 2 * i + 1;
-      r.a[i] = (float)(e < V ? x.v[e % V] : y.v[e % V]);
-      r.b[i] = (float)(o < V ? x.v[o % V] : y.v[o % V]);
+    for (int i = 0; i < V / 2; i++) {
+      r.a[i] = (float)x.v[2 * i];
+      r.b[i] = (float)x.v[2 * i + 1];
+      r.a[V / 2 + i] = (float)y.v[2 * i];
+      r.b[V / 2 + i] = (float)y.v[2 * i + 1];
     }
   } else {
 #pragma unroll
@@ -62,25 +71,38 @@ __device__ __forceinline__ Item<V> load_item(const T* head, const ItemPlace& p) 
   return r;
 }
 
-template <typename T, int V>
-__device__ __forceinline__ void store_item(T* head, const ItemPlace& p, const Item<V>& r) {
-  Vec<T, V> x, y;
-  if (p.interleaved) {
+// An item's two runs of values.
+template <int V>
+__device__ __forceinline__ void runs_of(const ItemPlace& p, const Item<V>& r, float (&x)[V], float (&y)[V]) {
+  if (V > 1 && p.interleaved) {
 #pragma unroll
-    for (int i = 0; i < V; i++) {
-      const int e = 2 * i, o = 2 * i + 1;
-      (e < V ? x.v[e % V] : y.v[e % V]) = (T)r.a[i];
-      (o < V ? x.v[o % V] : y.v[o % V]) = (T)r.b[i];
+    for (int i = 0; i < V / 2; i++) {
+      x[2 * i] = r.a[i];
+      x[2 * i + 1] = r.b[i];
+      y[2 * i] = r.a[V / 2 + i];
+      y[2 * i + 1] = r.b[V / 2 + i];
     }
   } else {
 #pragma unroll
     for (int i = 0; i < V; i++) {
-      x.v[i] = (T)r.a[i];
-      y.v[i] = (T)r.b[i];
+      x[i] = r.a[i];
+      y[i] = r.b[i];
     }
   }
-  *reinterpret_cast<Vec<T, V>*>(head + p.first) = x;
-  *reinterpret_cast<Vec<T, V>*>(head + p.second) = y;
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void store_item(T* head, const ItemPlace& p, const Item<V>& r) {
+  float x[V], y[V];
+  runs_of(p, r, x, y);
+  Vec<T, V> u, w;
+#pragma unroll
+  for (int i = 0; i < V; i++) {
+    u.v[i] = (T)x[i];
+    w.v[i] = (T)y[i];
+  }
+  *reinterpret_cast<Vec<T, V>*>(head + p.first) = u;
+  *reinterpret_cast<Vec<T, V>*>(head + p.second) = w;
 }
 
 template <int V>
@@ -88,13 +110,27 @@ struct Angles {
   Vec<float, V> c, s;
 };
 
-// The angles of item c from the table row (NULL: a position outside the table, all NaN).
+// The angles of an item's pairs from the table row (NULL: a position outside the table, all NaN).
 template <int V>
-__device__ __forceinline__ Angles<V> load_angles(const float* row, int c, int rot, bool inverse) {
+__device__ __forceinline__ Angles<V> load_angles(const float* row, const ItemPlace& p, int rot, bool inverse) {
   Angles<V> g;
   if (row) {
-    g.c = *reinterpret_cast<const Vec<float, V>*>(row + c * V);
-    g.s = *reinterpret_cast<const Vec<float, V>*>(row + rot / 2 + c * V);
+    if constexpr (V == 1) {
+      g.c.v[0] = row[p.pair0];
+      g.s.v[0] = row[rot / 2 + p.pair0];
+    } else {  // V / 2 at either place; in the half layout they are neighbours
+      using H = Vec<float, V / 2>;
+      const int p1 = p.interleaved ? p.pair1 : p.pair0 + V / 2;
+      const H c0 = *reinterpret_cast<const H*>(row + p.pair0), c1 = *reinterpret_cast<const H*>(row + p1);
+      const H s0 = *reinterpret_cast<const H*>(row + rot / 2 + p.pair0), s1 = *reinterpret_cast<const H*>(row + rot / 2 + p1);
+#pragma unroll
+      for (int i = 0; i < V / 2; i++) {
+        g.c.v[i] = c0.v[i];
+        g.c.v[V / 2 + i] = c1.v[i];
+        g.s.v[i] = s0.v[i];
+        g.s.v[V / 2 + i] = s1.v[i];
+      }
+    }
     if (inverse) {
 #pragma unroll
       for (int i = 0; i < V; i++) g.s.v[i] = -g.s.v[i];
