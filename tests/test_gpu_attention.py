@@ -82,6 +82,9 @@ class Case:
     ([64, 1, 20], [300, 301, 20], 4, 1, 64, 16, 37),
     ([129], [129], 2, 2, 112, 128, 1),
     ([100, 90], [400, 90], 16, 2, 128, 64, 64),
+    ([300, 17], [1500, 700], 8, 2, 128, 64, 0),
+    ([260], [2100], 2, 1, 64, 16, 300),
+    ([40, 1, 150], [1200, 1300, 400], 4, 2, 112, 32, 0),
 ])
 def test_attention(new, total, heads, kv_heads, D, page, window, dtype, out, workspace):
     Case(new, total, heads, kv_heads, D, page, dtype).run(window, TYPES[out], workspace=workspace)

@@ -37,6 +37,17 @@ def test_gemm(N, K, group, zero, dtype):
             _check(x, q, scale, z, group, patch.w4_gemm(x, w, out_dtype=od), f"M={M} {od}")
 
 
+@pytest.mark.parametrize("N,K,group,zero", [(4100, 256, 64, True), (8300, 288, 32, False), (13001, 128, 128, True),
+                                            (20000, 160, 32, True)])
+def test_many_bands(N, K, group, zero):
+    """Two to four bands a workgroup, and more than one round of the GPU."""
+    q, scale, z = _weight(N, K, group, zero, torch.bfloat16)
+    w = patch.w4_pack(q, scale, z, group)
+    for M in (1, 7, 20):
+        x = torch.randn(M, K, generator=torch.Generator().manual_seed(M)).bfloat16().cuda()
+        _check(x, q, scale, z, group, patch.w4_gemm(x, w), f"M={M}")
+
+
 def test_packed_bytes_are_as_stated():
     """The layout of patch_w4_pack, byte by byte, and its padding."""
     N, K, group = 20, 160, 32
