@@ -524,13 +524,15 @@ typedef struct {
  *   page_table     int32 [S][max_pages], rows page_table_row apart
  *   kv_lens        int32 [S];  cu_new  int32 [S + 1], not decreasing, from 0
  *   table          float32 [context][rot] of patch_rope_table, or NULL
- * A page that receives tokens must belong to one sequence alone.  New tokens
+ * A page that receives tokens must stand in the table of one sequence alone,
+ * and once in it; sequences may share pages that are full.  New tokens
  * whose place is negative, behind max_pages, or in a page outside 0 ..
  * pages - 1 are not stored; positions outside the table make the rotated
  * elements NaN (q) or stored as NaN (k); tokens outside 0 .. T - 1 are not
  * read.
- * Errors: PATCH_ERR_SHAPE (sizes as above, rot odd, < 2 or > dim),
- * PATCH_ERR_INVALID_ARG (null pointers, misalignment, dtype, layout).
+ * Errors: PATCH_ERR_SHAPE (sizes as above, T from 2^30, S over 4096, rot odd,
+ * < 2 or > dim), PATCH_ERR_INVALID_ARG (null pointers, misalignment, dtype,
+ * layout).
  */
 typedef struct {
   int64_t dtype, layout;
@@ -567,14 +569,16 @@ patch_status patch_kv_append(const patch_kv_append_args* args, const patch_kv_ca
  * page number outside 0 .. pages - 1 among the pages it sees, or a length
  * beyond max_pages * page: out and lse NaN.  Keys, values and scales that a
  * token does not see do not reach its output, NaN among them.  Scales must
- * be finite.  Rows of out and lse behind cu_new[S] are left as they are.
+ * be finite and not negative.  Rows of out and lse behind cu_new[S] are left
+ * as they are.
  *   workspace: patch_attention_workspace_bytes(...) bytes of scratch, 16-byte
  * aligned, contents of no matter before and after; calls that may run at the
  * same time need workspaces of their own.  NULL or a smaller one: no work is
  * split, same results but for rounding.
  * Errors: PATCH_ERR_SHAPE (cache sizes, heads no multiple of kv_heads, S over
- * 4096), PATCH_ERR_INVALID_ARG (null pointers, misalignment, dtypes, scale not
- * finite, window < 0).
+ * 4096, T or T heads / kv_heads from 2^30), PATCH_ERR_INVALID_ARG (null
+ * pointers, misalignment, dtypes, scale not finite or above 1e30 in size,
+ * window < 0).
  */
 typedef struct {
   int64_t dtype, out_dtype;

@@ -129,7 +129,7 @@ struct Seq {
 };
 __device__ __forceinline__ Seq seq_of(const Args& a, int s) {
   Seq q;
-  const int e = min(a.cu[s + 1], a.T), len = a.lens[s];
+  const int e = max(min(a.cu[s + 1], a.T), 0), len = a.lens[s];
   q.c0 = max(a.cu[s], 0);
   q.n = max(e - q.c0, 0);
   q.past = max(len, -0x40000000) - q.n;
@@ -328,7 +328,9 @@ struct LaneLine {
   int from, to, total;
   __device__ __forceinline__ explicit LaneLine(int n) : to(wave_scan(n)) {
     from = to - n;
-    total = lane_of(to, 63);
+    // cu_new that decreases can count tokens until the sum overflows (the first
+    // sum that does is negative): nothing is on the line then.
+    total = __any(to < 0) ? 0 : lane_of(to, 63);
   }
   __device__ __forceinline__ Place find(int u) const {
     const int s = __builtin_ctzll(__ballot(to > u));  // the first that ends behind u
@@ -346,18 +348,24 @@ struct LdsLine {
     const int tid = (int)threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int each = (S + threads_of<Body> - 1) / threads_of<Body>, s1 = min((tid + 1) * each, S);
     int mine = 0;
+    bool bad = false;  // the sum overflows, see LaneLine
     for (int s = tid * each; s < s1; s++) {
       line[s] = cost(s);
       mine += line[s];
+      bad |= mine < 0;
     }
     const int upto = wave_scan(mine);
-    if (lane == 63) wave_sum[wave] = upto;
+    bad = __any(bad || upto < 0);
+    if (lane == 63) wave_sum[wave] = bad ? -1 : upto;
     __syncthreads();
     int at = upto - mine;
+    bad = false;
     for (int w = 0; w < Body::kWaves; w++) {
       if (w < wave) at += wave_sum[w];
       total += wave_sum[w];
+      bad |= wave_sum[w] < 0 || total < 0;
     }
+    if (bad) total = 0;
     for (int s = tid * each; s < s1; s++) {
       const int n = line[s];
       line[s] = at;
@@ -448,7 +456,7 @@ __global__ __launch_bounds__(threads_of<Body>, Body::kPerCu* Body::kWaves / 4) v
   const bool even = line.total <= (int)gridDim.x;  // a piece a workgroup
   if (!even) line = make(false);
   const Cut cut(line.total, even ? line.total : (int)gridDim.x);
-  if ((int)blockIdx.x >= cut.pieces) return;
+  if (line.total == 0 || (int)blockIdx.x >= cut.pieces) return;
   int u = cut.start((int)blockIdx.x);
   const int u_end = cut.start((int)blockIdx.x + 1);
   while (u < u_end) {

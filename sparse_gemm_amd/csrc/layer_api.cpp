@@ -71,8 +71,8 @@ patch_status check_cache(const patch_kv_cache* c) {
 patch_status check_seqs(int64_t T, int64_t S, int64_t heads, const patch_kv_cache* c, int64_t max_pages, int64_t row,
                         const void* table, const void* lens, const void* cu) {
   if (T < 0 || S < 0) return fail(PATCH_ERR_INVALID_ARG, "T=%lld or S=%lld is negative", (long long)T, (long long)S);
-  if (T >= kMaxSize || S > patch::kMaxSeqs)
-    return fail(PATCH_ERR_SHAPE, "T=%lld S=%lld: at most 2^31 - 1 tokens and %lld sequences", (long long)T, (long long)S,
+  if (T >= kMaxSize / 2 || S > patch::kMaxSeqs)
+    return fail(PATCH_ERR_SHAPE, "T=%lld S=%lld: less than 2^30 tokens and at most %lld sequences", (long long)T, (long long)S,
                 (long long)patch::kMaxSeqs);
   if (heads < 1 || heads > 65536 || heads % c->kv_heads)
     return fail(PATCH_ERR_SHAPE, "heads=%lld must be a multiple of kv_heads=%lld", (long long)heads,
@@ -187,10 +187,9 @@ patch_status patch_attention(const patch_attention_args* a, const patch_kv_cache
   if ((s = check_seqs(a->T, a->S, a->heads, c, a->max_pages, a->page_table_row, a->page_table_dev, a->kv_lens_dev,
                       a->cu_new_dev)))
     return s;
-  if (!std::isfinite(a->scale) || !std::isfinite((float)a->scale))
-    return fail(PATCH_ERR_INVALID_ARG, "scale must be finite");
+  if (!(std::fabs(a->scale) <= 1e30)) return fail(PATCH_ERR_INVALID_ARG, "scale must be finite, at most 1e30 in size");
   if (a->window < 0) return fail(PATCH_ERR_INVALID_ARG, "window=%lld is negative", (long long)a->window);
-  if (a->T * (a->heads / c->kv_heads) >= kMaxSize)
+  if (a->T * (a->heads / c->kv_heads) >= kMaxSize / 2)
     return fail(PATCH_ERR_SHAPE, "T=%lld times %lld heads a cache head is too large", (long long)a->T,
                 (long long)(a->heads / c->kv_heads));
   if (workspace_bytes > 0 && (!workspace_dev || !aligned(workspace_dev, 16)))

@@ -698,6 +698,14 @@ def _heads(t, name: str, dtype, T, H, D, index):
     return t.data_ptr(), st[0], st[1], s[1]
 
 
+def _rows_out(t, name: str, dtype, T, H, D, index):
+    """_heads of a tensor that is written."""
+    p, st, sh, _ = _heads(t, name, dtype, T, H, D, index)
+    if (st == 0 and T > 1) or (sh == 0 and H > 1):
+        raise ValueError(f"{name} overlaps itself")
+    return p, st, sh
+
+
 def _index(t, name: str, n: int, index):
     if not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or t.dim() != 1 or t.shape[0] != n or (
             n > 1 and not t.is_contiguous()):
@@ -766,10 +774,11 @@ def rope(x: torch.Tensor, positions: torch.Tensor, table: torch.Tensor, layout: 
     tp, context, rot = _table_of(table, index)
     if not rot:
         raise ValueError("table must be a tensor with rot > 0 columns")
-    _need_device(index)
     if out is None:
+        _need_device(index)
         out = torch.empty((T, H, D), dtype=dt, device=x.device)
-    op, ot, oh, _ = _heads(out, "out", dt, T, H, D, index)
+    op, ot, oh = _rows_out(out, "out", dt, T, H, D, index)
+    _need_device(index)
     _call(index, lib.patch_rope,
           _ROPE_ARGS.pack(dtype, _LAYOUTS[layout], bool(inverse), T, H, D, rot, context, xp, xt, xh, op, ot, oh, pos, tp))
     return out
@@ -863,7 +872,7 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, cache: KVCache, page_table: torc
         qp, qt, qh, heads = _heads(q, "q", dt, T, None, D, index)
         if q_out is None:
             q_out = torch.empty((T, heads, D), dtype=dt, device=k.device)
-        op, ot, oh, _ = _heads(q_out, "q_out", dt, T, heads, D, index)
+        op, ot, oh = _rows_out(q_out, "q_out", dt, T, heads, D, index)
     elif q_out is not None:
         raise ValueError("q_out without q")
     _call(index, lib.patch_kv_append,
@@ -902,7 +911,7 @@ def attention(q: torch.Tensor, cache: KVCache, page_table: torch.Tensor, kv_lens
         _check_out_dtype(od, dt)
     if out is None:
         out = torch.empty((T, H, D), dtype=od, device=q.device)
-    op, ot, oh, _ = _heads(out, "out", od, T, H, D, index)
+    op, ot, oh = _rows_out(out, "out", od, T, H, D, index)
     lp = 0
     if lse is not None:
         _check_dev(lse, "lse", torch.float32, (T, H))

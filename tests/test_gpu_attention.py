@@ -213,6 +213,47 @@ def test_graph_follows_lengths():
     c.check(out, lse)
 
 
+def test_graph_of_chunks_follows_lengths():
+    c = Case([150, 90], [700, 400], 4, 2, 128, 64, "bf16")
+    full, lens, pt, cu = c.lens.clone(), c.lens.cuda(), c.pt.cuda(), c.cu.cuda()
+    out = torch.empty_like(c.q)
+    ws = torch.randint(0, 256, (patch.attention_workspace_bytes(240, 2, 4, 2, 128),), dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        patch.attention(c.q, c.cache, pt, lens, cu, out=out, workspace=ws)
+    for by in (0, 130, 200, 0):
+        lens.copy_(full - by)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, patch.attention(c.q, c.cache, pt, lens, cu)), by
+
+
+def test_offsets_beyond_32_bits():
+    """Pages whose bytes lie behind the first 4 GiB of a cache, appended to and
+    attended to by one token and by a chunk."""
+    pages, hk, page, D = 70000, 4, 128, 128
+    cache = patch.kv_cache(pages, hk, D, page)
+    assert cache.k.numel() > 1 << 32
+    g = torch.Generator().manual_seed(0)
+    table = patch.rope_table(512, D)
+    for n in (1, 140):
+        total, start = 300, 300 - n
+        pt = torch.tensor([[pages - 1, 0, pages - 7]], dtype=torch.int32, device="cuda")
+        small = patch.kv_cache(3, hk, D, page)
+        spt = torch.tensor([[0, 1, 2]], dtype=torch.int32, device="cuda")
+        outs = []
+        x = torch.randn(total, 3 * hk, D, generator=g).bfloat16().cuda()
+        for c, t in ((cache, pt), (small, spt)):
+            for at, m in ((0, start), (start, n)):
+                lens = torch.tensor([at + m], dtype=torch.int32, device="cuda")
+                cu = torch.tensor([0, m], dtype=torch.int32, device="cuda")
+                y = x[at:at + m]
+                q = patch.kv_append(y[:, :hk], y[:, hk:2 * hk], c, t, lens, cu, table=table, q=y[:, 2 * hk:])
+            outs.append(patch.attention(q, c, t, lens, cu))
+        assert torch.equal(outs[0], outs[1]) and torch.equal(cache.k.view(torch.uint8)[pages - 1], small.k.view(torch.uint8)[0])
+
+
 def test_two_streams_at_once():
     a, b = Case([1, 1], [2500, 900], 8, 2, 128, 64, "bf16"), Case([1], [3100], 8, 2, 128, 64, "bf16", seed=5)
     want = [c.run(check=False)[0] for c in (a, b)]
@@ -234,6 +275,8 @@ def test_many_sequences():
     new = [1 if i % 7 else 0 for i in range(300)]
     total = [(i * 37) % 90 + 1 for i in range(300)]
     Case(new, total, 2, 1, 32, 16, "bf16").run()
+    new = [(i * 29) % 90 for i in range(70)]  # and chunks of them
+    Case(new, [n + (i * 53) % 200 for i, n in enumerate(new)], 2, 1, 64, 16, "f16").run()
 
 
 def test_no_tokens():

@@ -68,7 +68,7 @@ BAD_CACHE = [(dict(page=24), "SHAPE"), (dict(page=8), "SHAPE"), (dict(page=256),
              (dict(dim=272), "SHAPE"), (dict(dim=0), "SHAPE"), (dict(pages=0), "SHAPE"), (dict(heads=0), "SHAPE"),
              (dict(k=0), "INVALID_ARG"), (dict(vs=0), "INVALID_ARG"), (dict(v=P + 8), "INVALID_ARG"),
              (dict(ks=P + 2), "INVALID_ARG")]
-BAD_SEQS = [(dict(T=-1), "INVALID_ARG"), (dict(S=-1), "INVALID_ARG"), (dict(S=4097), "SHAPE"), (dict(T=1 << 31), "SHAPE"),
+BAD_SEQS = [(dict(T=-1), "INVALID_ARG"), (dict(S=-1), "INVALID_ARG"), (dict(S=4097), "SHAPE"), (dict(T=1 << 30), "SHAPE"),
             (dict(heads=3), "SHAPE"), (dict(heads=0), "SHAPE"), (dict(max_pages=-1), "SHAPE"),
             (dict(max_pages=1 << 28, row=1 << 28), "SHAPE"), (dict(row=3), "SHAPE"), (dict(pt=0), "INVALID_ARG"),
             (dict(lens=0), "INVALID_ARG"), (dict(cu=0), "INVALID_ARG"), (dict(cu=P + 2), "INVALID_ARG"),
@@ -104,7 +104,7 @@ def test_append_refuses(change, status):
     (dict(scale=1e300), "INVALID_ARG"), (dict(window=-1), "INVALID_ARG"), (dict(q=0), "INVALID_ARG"),
     (dict(out=0), "INVALID_ARG"), (dict(out=P + 1), "INVALID_ARG"), (dict(lse=P + 2), "INVALID_ARG"),
     (dict(ws=(0, 64)), "INVALID_ARG"), (dict(ws=(P + 8, 64)), "INVALID_ARG"),
-    (dict(T=(1 << 31) - 1, heads=4), "SHAPE")])
+    (dict(T=(1 << 30) - 1, heads=8), "SHAPE"), (dict(scale=-1e31), "INVALID_ARG")])
 def test_attention_refuses(change, status):
     assert _attend(**change) == "PATCH_ERR_" + status
 
@@ -174,6 +174,8 @@ def test_binding_checks_types_and_shapes():
                      (lambda: patch.KVCache(k, v, ks, vs), "device")):
         with pytest.raises(ValueError, match=msg):
             bad()
+    with pytest.raises(ValueError, match="itself"):
+        patch.rope(x, pos, tab, out=x[:, :1].expand(3, 2, 32))
     for fn in (patch.kv_append, patch.attention):
         with pytest.raises(ValueError, match="KVCache"):
             fn(x, x, *(None,) * 4) if fn is patch.kv_append else fn(x, None, None, None, None)
