@@ -44,8 +44,16 @@
 // sees them all.  Two may; they write the same values.  A flag is a 64-bit
 // value of the launch, put back to 0 by who joins, so the workspace's
 // contents do not matter and a captured launch replays.
+//
+// Bound by the cache's bytes from a few megabytes on, below that by the chain
+// lengths -> page table -> scales -> keys -> parts -> join, which is a handful
+// of trips to memory.  Heads of 128, GPU time: 48 sequences of 200 to 4000
+// tokens, 8 cache heads, 224 MB in 53.6 us (4.2 TB/s); two of 100 000 to 130
+// 000, 486 MB in 110 us (4.4 TB/s; a copy of 1 GiB reaches 5.1); one of 700,
+// 32 cache heads, 5.7 MB in 11.4 us.
 #include <algorithm>
 #include <atomic>
+#include <chrono>
 #include <random>
 
 #include "attention_common.h"
@@ -311,7 +319,11 @@ __device__ __forceinline__ void do_step(const Args& a, const Task& task, int ste
 template <bool BF16, int DP, int R>
 struct Few {
   static constexpr bool kBf16 = BF16;
-  static constexpr int kWaves = patch::kWaves, kDim = DP, kRows = 16 * R, kStep = patch::kStep, kMinSteps = 8, kTaskCost = 8;
+  static constexpr int kWaves = patch::kWaves, kDim = DP, kRows = 16 * R, kStep = patch::kStep;
+  // Measured: pieces of at least 8 steps, 4 sequences of 1500 tokens 12.6 us,
+  // of 4 steps 15.8, of 16 steps 13.7.  A task's own cost of 16 steps, 48
+  // sequences of 200 to 4000 tokens 40.5 us, of 8 steps 42.3, of 2 steps 49.7.
+  static constexpr int kMinSteps = 8, kTaskCost = 16;
   static constexpr int kPerCu = R == 1 && DP <= 128 ? 2 : 1;
   static constexpr int kLds = kWaves * kRows * (DP + 4) + kWaves * kRows * 2 + kWaves;
 
@@ -400,10 +412,15 @@ struct Few {
 }
 };
 
-// Many rows a sequence on average: attention_chunk.hip.
-bool many_rows(int64_t T, int64_t S, int64_t group, int64_t dim) { return dim <= 128 && T * group > 32 * S; }
+// Many rows a sequence on average: attention_chunk.hip, whose workgroup reads a
+// key once for 128 rows.  8 sequences of 4096 keys, 32 query and 8 cache heads
+// of 128, this file's against that one's: 64 rows 41 us to 51, 96 rows 64 to
+// 57, 256 rows 115 to 85.
+bool many_rows(int64_t T, int64_t S, int64_t group, int64_t dim) { return dim <= 128 && T * group > 64 * S; }
 
-// Sixteens of rows of a task, by the rows a sequence has on average.
+// Sixteens of rows of a task, by the rows a sequence has on average.  As above,
+// one against two: 4 rows 23.1 us to 25.6, 16 rows 25.4 to 26.9, 24 rows 32.9
+// to 29.6, 64 rows 56 to 41.
 int tile_rows(int64_t T, int64_t S, int64_t group, int64_t dim) { return T * group <= 16 * S || dim > 128 ? 1 : 2; }
 
 template <bool BF16>
@@ -421,9 +438,13 @@ namespace attn {
 // A value of this launch for the flags: a counter mixed with a random salt of
 // the process (splitmix64's finaliser), never 0.
 uint64_t launch_token() {
-  static const uint64_t salt = [] {
-    std::random_device rd;
-    return ((uint64_t)rd() << 32) ^ (uint64_t)rd();
+  static const uint64_t salt = []() -> uint64_t {
+    try {
+      std::random_device rd;
+      return ((uint64_t)rd() << 32) ^ (uint64_t)rd();
+    } catch (...) {  // no source of entropy
+      return (uint64_t)std::chrono::steady_clock::now().time_since_epoch().count();
+    }
   }();
   static std::atomic<uint64_t> counter{1};
   uint64_t z = salt + 0x9e3779b97f4a7c15ull * counter.fetch_add(1, std::memory_order_relaxed);

@@ -2,16 +2,27 @@
 // tokens a sequence (prompts and their chunks).
 //
 // Here the matrix cores and the exponentials bound the work, not the cache:
-// every row tile reads the same keys, mostly from L2.  So the four waves of a
+// every row tile reads the same keys, mostly from L2.  So the eight waves of a
 // workgroup have 16 R rows each and share the keys: a tile of 128 keys is
-// loaded once, each wave widening 32 of them into LDS as ready matrix
+// loaded once, each wave widening 16 of them into LDS as ready matrix
 // operands (lane order, 16 bytes a lane: reads and writes without bank
-// conflicts), and every wave then runs all 128 against its rows.  The next
-// tile's bytes are in registers by then.  Rows are a wave's own, so nothing is
-// joined at the end; two workgroups a CU fill each other's waits.
+// conflicts), and every wave then runs all 128 against its rows.  LDS holds two
+// tiles (128 KB at 128 elements, so one workgroup a CU): one is used while the
+// next is filled, whose bytes were loaded a tile earlier; one barrier a tile.
+// Rows are a wave's own, so nothing is joined at a task's end.
 //
 // The products, the running maximum and sum, and the order of the keys inside
 // an operand are those of attention.hip.
+//
+// Three sequences, 700 to 1100 new tokens behind 1500 to 5000, 32 query and 8
+// cache heads of 128: 152 GFLOP in 253 us, 603 TFLOP/s, where a large bf16
+// product reaches 1239.  A wave's matrix instructions take 74 us of that and
+// its other arithmetic (exponentials, widening, maxima, sums) 116, and two
+// waves a SIMD (256 registers each) overlap them little.  Measured instead:
+// two workgroups of four waves with a tile each, 16 rows a wave at four waves a
+// SIMD (434 us, registers spill), 64 keys of scores before the exponentials
+// (263 us against 262 then), wave priorities around the second product (271)
+// and prescribed interleavings of matrix and other instructions (276 to 300).
 #include "attention_common.h"
 
 namespace patch {
@@ -29,7 +40,12 @@ __device__ __forceinline__ void meet() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts
 template <bool BF16, int DP, int R, bool FULL>
 struct Chunk {
   static constexpr bool kBf16 = BF16;
-  static constexpr int kWaves = 8, kDim = DP, kRows = kWaves * 16 * R, kStep = kTile, kMinSteps = 4, kTaskCost = 2;
+  static constexpr int kWaves = 8, kDim = DP, kRows = kWaves * 16 * R, kStep = kTile;
+  // Measured: pieces of at least 4 tiles, a prompt of 600 tokens 53.6 us, of 2
+  // tiles 55.3, of 8 tiles 51.2.  A task's own cost (its rows' q, the first
+  // tiles' way into LDS, its part) of 6 tiles, prompts of 1500, 300, 2000 and
+  // 800 tokens 183 us, of 2 tiles 212, of 12 tiles 199.
+  static constexpr int kMinSteps = 4, kTaskCost = 6;
   static constexpr int kPerCu = 1;
   static constexpr int kFrags = DP / 16;                        // operands (1 KB) of 32 keys, of K as of V
   static constexpr int kBuf = kTile / 32 * 2 * kFrags * 64;       // 16-byte words of a tile
@@ -409,9 +425,10 @@ struct Chunk {
 };
 
 
-// Rows of a wave in sixteens, by the rows a sequence has on average: a task of
-// 256 rows would be half empty below 128.
-int wave_rows(int64_t T, int64_t S, int64_t group) { return T * group <= 128 * S ? 1 : 2; }
+// Rows of a wave in sixteens, by the rows a sequence has on average.  8
+// sequences of 4096 keys, 32 query and 8 cache heads of 128, one against two:
+// 128 rows 63 us to 78, 256 rows 85 to 101, 512 rows 140 to 127.
+int wave_rows(int64_t T, int64_t S, int64_t group) { return T * group <= 256 * S ? 1 : 2; }
 
 template <bool BF16, int R>
 hipError_t by_dim(Args& a, void* ws, uint64_t ws_bytes, hipStream_t s) {

@@ -3,9 +3,10 @@
 //
 // A kernel's body says how a workgroup attends to a range of keys for the
 // rows of one task:
-//   kBf16, kWaves (of a workgroup), kDim (elements of a head, padded), kRows (of a task), kStep (keys of
-//   a step), kMinSteps (of a workgroup, at least), kTaskCost (what a task costs
-//   beside its steps, in steps), kPerCu (workgroups a CU), kLds (its LDS, floats),
+//   kBf16, kWaves (of a workgroup), kDim (elements of a head, padded), kRows (of
+//   a task), kStep (keys of a step), kMinSteps (of a workgroup, at least),
+//   kTaskCost (what a task costs beside its steps, in steps), kPerCu
+//   (workgroups a CU), kLds (its LDS, floats),
 //   run(a, sq, task, s, h, begin, end, part, lds): the steps begin .. end - 1.
 //   Of a task in one part the rows are stored, else o / l, m and l go to this
 //   workgroup's slot of the workspace.

