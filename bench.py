@@ -27,6 +27,7 @@ from __future__ import annotations
 
 import argparse
 import ctypes
+import dataclasses
 import hashlib
 import json
 import os
@@ -1261,9 +1262,94 @@ def fused_set(kind, si, Ms, steps, warmup, batches):
     return out
 
 
+def attention_set(steps, warmup, batches, shapes=((1, 1, 700), (16, 1, 2000), (64, 1, 2000), (1, 2048, 0))):
+    """A LLaMA-2-7B attention block on (sequences, new tokens each, tokens
+    before) -- hidden size 4096, 32 heads of 128, pages of 64: q/k/v projections
+    packed as one blob (sweep weights, half the tiles 2:4), the keys' and values'
+    append to the paged 8-bit cache with the rotation of q and k, attention, and
+    the output projection with 4-bit weights in groups of 128.  Graph replays of
+    the whole block and of each part; weights and caches are rotated over.
+    Roofline: the bytes of the weights, of the cache that is read and of the
+    tokens, or the products' time on the matrix cores."""
+    import torch
+
+    from sparse_gemm_amd import inputs, patch
+
+    H, D, page, hidden, group = 32, 128, 64, 4096, 128
+    cfg = inputs.CONFIGS["sweep"]
+    ps = [inputs.make_weights(cfg, mi, 2) for mi in range(3)]
+    tdt = torch.bfloat16
+    qkv = patch.pack_concat([dev_bits(p.w, tdt) for p in ps], [p.tile_map for p in ps],
+                            [torch.from_numpy(p.mask).cuda() for p in ps])
+    blobs = rotate(qkv.blob, qkv.nbytes)
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    wo = (0.02 * torch.randn(hidden, H * D, device="cuda", generator=gen)).to(tdt)
+    w4 = patch.w4_pack(*patch.w4_quantize(wo, group), group)
+    w4s = [dataclasses.replace(w4, packed=b) for b in rotate(w4.packed, w4.packed.numel())]
+    out = []
+    for S, new, past in shapes:
+        total, T = past + new, S * new
+        per_seq = -(-total // page)
+        set_bytes = S * per_seq * page * 2 * H * D
+        sets = max(1, min(64, -(-ROTATE_BYTES // set_bytes)))
+        cache = patch.kv_cache(sets * S * per_seq, H, D, page)
+        for c in (cache.k, cache.v):
+            c.view(torch.uint8).random_(0x20, 0x40, generator=gen)
+        cache.k_scale.fill_(2.0 ** -4)
+        cache.v_scale.fill_(2.0 ** -4)
+        order = torch.randperm(sets * S * per_seq, device="cuda", generator=gen).int()
+        tables = list(order.view(sets, S, per_seq).contiguous())
+        lens = torch.full((S,), total, dtype=torch.int32, device="cuda")
+        cu = (torch.arange(S + 1, device="cuda") * new).int()
+        table = patch.rope_table(total, D)
+        X = (0.05 * torch.randn(T, hidden, device="cuda", generator=gen)).to(tdt)
+        Y = torch.empty((T, 3 * H * D), dtype=tdt, device="cuda")
+        y3 = Y.view(T, 3 * H, D)
+        q, k, v = y3[:, :H], y3[:, H:2 * H], y3[:, 2 * H:]
+        o = torch.empty((T, H, D), dtype=tdt, device="cuda")
+        Z = torch.empty((T, hidden), dtype=tdt, device="cuda")
+        aws = torch.empty(patch.attention_workspace_bytes(T, S, H, H, D), dtype=torch.uint8, device="cuda")
+
+        def f_qkv(i):
+            patch.gemm(X, patch.PackedWeight(blobs[i % len(blobs)], qkv.desc), out=Y, workspace=ws_gemm(qkv.desc, T))
+
+        def f_append(i):
+            patch.kv_append(k, v, cache, tables[i % sets], lens, cu, table=table, q=q, q_out=q)
+
+        def f_attend(i):
+            patch.attention(q, cache, tables[i % sets], lens, cu, out=o, workspace=aws)
+
+        def f_out(i):
+            patch.w4_gemm(o.view(T, H * D), w4s[i % len(w4s)], out=Z)
+
+        def f_block(i):
+            f_qkv(i)
+            f_append(i)
+            f_attend(i)
+            f_out(i)
+
+        calls = [("block", f_block), ("qkv", f_qkv), ("append", f_append), ("attention", f_attend), ("w4", f_out)]
+        _, per = time_graphs(calls, steps, warmup, batches)
+        us = {name: median(per[name]) * 1e3 for name, _ in calls}
+        keys = S * (new * past + new * (new + 1) // 2)  # query-key pairs of a head
+        token_bytes = 2 * T * (2 * hidden + 10 * H * D) + 2 * T * H * D
+        nbytes = qkv.nbytes + w4.packed.numel() + S * total * 2 * H * D + token_bytes
+        flops = 2.0 * T * hidden * 3 * H * D + 4.0 * keys * H * D + 2.0 * T * H * D * hidden
+        t_hbm, t_mma = nbytes / (HBM_PEAK_GBS * 1e9), flops / (MFMA_PEAK_BF16_TFLOPS * 1e12)
+        out.append(dict(config="attention_block", sequences=S, new_tokens=new, past_tokens=past, us=us["block"],
+                        us_qkv=us["qkv"], us_append=us["append"], us_attention=us["attention"], us_w4=us["w4"],
+                        algorithmic_bytes=nbytes, flops=flops,
+                        roofline_bound="hbm" if t_hbm >= t_mma else "mfma",
+                        roofline_frac=max(t_hbm, t_mma) / (us["block"] * 1e-6)))
+        del cache, tables
+        torch.cuda.empty_cache()
+    return out
+
+
 def write_report(path, steps, warmup, batches):
-    """Every workload: decode, prefill MLP, the sparsity sweep and the 13B
-    imbalanced shapes; one JSON line per (matrix, s, M).  Each time is the
+    """Every workload: decode, prefill MLP, the sparsity sweep, the 13B
+    imbalanced shapes, 4:8 tiles, fine masks, the sampler, fused projections
+    and the attention block; one JSON line per (matrix, s, M).  Each time is the
     median of `batches` batches of `steps` launches (min and max beside it)."""
     from sparse_gemm_amd import inputs
 
@@ -1318,6 +1404,13 @@ def write_report(path, steps, warmup, batches):
                     print(f"[report] fused {kind} s={rec['sparse_tile_fraction']:.2f} M={M}: {rec['us']:.2f} us, "
                           f"x{rec['speedup_vs_unfused']:.3f} vs unfused, x{rec['speedup_vs_dense']:.3f} vs dense",
                           flush=True)
+        for rec in attention_set(steps, warmup, batches):
+            f.write(json.dumps(rec) + "\n")
+            f.flush()
+            print(f"[report] attention block, {rec['sequences']} x {rec['new_tokens']} tokens after "
+                  f"{rec['past_tokens']}: {rec['us']:.2f} us (qkv {rec['us_qkv']:.2f}, append {rec['us_append']:.2f}, "
+                  f"attention {rec['us_attention']:.2f}, w4 {rec['us_w4']:.2f}), roofline {rec['roofline_frac']:.2f}",
+                  flush=True)
 
 
 if __name__ == "__main__":
