@@ -897,7 +897,8 @@ def main():
     ap.add_argument("--report-steps", type=int, default=100, help="launches per timed batch in the report")
     ap.add_argument("--report-batches", type=int, default=10, help="timed batches per point in the report (median)")
     ap.add_argument("--workload", default="prefill_mlp",
-                    choices=["prefill_mlp", "decode", "imbalanced_13b", "sampler", "fine_mask", "n48", "tile64"],
+                    choices=["prefill_mlp", "decode", "imbalanced_13b", "sampler", "fine_mask", "n48", "tile64",
+                             "attention_block"],
                     help="prefill_mlp (default: the headline line); the others print that workload's lines, "
                          "for profiling")
     ap.add_argument("--hybrid-only", action="store_true",
@@ -941,8 +942,9 @@ def main():
         for rec in q64_set(args.steps, args.warmup):
             print(json.dumps(rec), flush=True)
         return
-    if args.workload in ("sampler", "fine_mask", "n48"):
-        fn = {"sampler": sampler_set, "fine_mask": fine_set, "n48": n48_set}[args.workload]
+    if args.workload in ("sampler", "fine_mask", "n48", "attention_block"):
+        fn = {"sampler": sampler_set, "fine_mask": fine_set, "n48": n48_set,
+              "attention_block": attention_set}[args.workload]
         for rec in fn(args.steps, args.warmup, 1):
             print(json.dumps(rec), flush=True)
         return
