@@ -270,7 +270,6 @@ __global__ __launch_bounds__(256) void k_w4_quantize(int64_t N, int64_t K, int G
 template <bool BF16, bool OUT_F32, int MT, int RB, int G, bool ZERO>
 hipError_t go(const W4Args& a, hipStream_t s) {
   const int64_t my = (a.M + 16 * MT - 1) / (16 * MT);
-  if (my > 65535) return hipErrorInvalidValue;
   // a wave takes two blocks or more where there are enough
   const int waves = std::max(1, std::min(kMaxWaves, a.blocks / 2));
   const size_t lds = (size_t)waves * RB * MT * 1024;
@@ -290,21 +289,26 @@ hipError_t by_group(const W4Args& a, hipStream_t s) {
     default: return by_zero<BF16, OUT_F32, MT, RB, 128>(a, s);
   }
 }
+template <bool BF16, bool OUT_F32, int MT>
+hipError_t by_bands(const W4Args& a, hipStream_t s) {
+  // A workgroup reads its tokens whole from L2 and has a CU to itself: as many
+  // bands as make one round of the GPU, so that tokens are read seldom and no
+  // second round waits, up to what its registers hold.  11008 x 4096 (688
+  // bands), 16 tokens: 16.1 us with two bands, 11.5 with three, 12.9 with four;
+  // 4096 x 4096 (256 bands), 64 tokens: 22.9 us with one, 14.0 with two, 15.4
+  // with four; 2048 tokens: 598 us with one, 346 with two, 209 with four.
+  const int64_t wide = (a.M + 16 * MT - 1) / (16 * MT);
+  switch (std::min<int64_t>((a.bands * wide + cu_count() - 1) / cu_count(), 4)) {
+    case 0:
+    case 1: return by_group<BF16, OUT_F32, MT, 1>(a, s);
+    case 2: return by_group<BF16, OUT_F32, MT, 2>(a, s);
+    case 3: return by_group<BF16, OUT_F32, MT, 3>(a, s);
+    default: return by_group<BF16, OUT_F32, MT, 4>(a, s);
+  }
+}
 template <bool BF16, bool OUT_F32>
 hipError_t by_tokens(const W4Args& a, hipStream_t s) {
-  // A workgroup of three or four bands has a CU to itself, and what does not fit
-  // in one round waits for a second: as many bands as make one round.  11008 x
-  // 4096 (688 bands), 16 tokens: 16.1 us with two bands, 11.5 with three, 12.9
-  // with four.
-  const int round = (a.bands + cu_count() - 1) / cu_count();
-  if (a.M > 16) return round <= 1 ? by_group<BF16, OUT_F32, 2, 1>(a, s) : by_group<BF16, OUT_F32, 2, 2>(a, s);
-  switch (round) {
-    case 0:
-    case 1: return by_group<BF16, OUT_F32, 1, 1>(a, s);
-    case 2: return by_group<BF16, OUT_F32, 1, 2>(a, s);
-    case 3: return by_group<BF16, OUT_F32, 1, 3>(a, s);
-    default: return by_group<BF16, OUT_F32, 1, 4>(a, s);
-  }
+  return a.M > 16 ? by_bands<BF16, OUT_F32, 2>(a, s) : by_bands<BF16, OUT_F32, 1>(a, s);
 }
 
 }  // namespace
@@ -343,16 +347,21 @@ hipError_t launch_w4_gemm(bool bf16, bool out_f32, bool zero, int64_t N, int64_t
   a.w = packed;
   a.scale = packed + scale_offset(N, K);
   a.zero = zero ? packed + zero_offset(N, K, group) : nullptr;
-  a.X = X;
-  a.Y = Y;
-  a.M = M;
   a.N = N;
   a.K = K;
   a.bands = (int)n_bands(N);
   a.blocks = (int)n_blocks(K);
   a.group = group;
-  if (bf16) return out_f32 ? by_tokens<true, true>(a, s) : by_tokens<true, false>(a, s);
-  return out_f32 ? by_tokens<false, true>(a, s) : by_tokens<false, false>(a, s);
+  constexpr int64_t kMost = int64_t(32) * 65535;  // rows of a launch, by the grid's second extent
+  for (int64_t m = 0; m < M; m += kMost) {
+    a.X = reinterpret_cast<const uint16_t*>(X) + m * K;
+    a.Y = reinterpret_cast<char*>(Y) + m * N * (out_f32 ? 4 : 2);
+    a.M = std::min(M - m, kMost);
+    const hipError_t e = bf16 ? (out_f32 ? by_tokens<true, true>(a, s) : by_tokens<true, false>(a, s))
+                              : (out_f32 ? by_tokens<false, true>(a, s) : by_tokens<false, false>(a, s));
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace patch

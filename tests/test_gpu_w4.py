@@ -48,6 +48,26 @@ def test_many_bands(N, K, group, zero):
         _check(x, q, scale, z, group, patch.w4_gemm(x, w), f"M={M}")
 
 
+@pytest.mark.parametrize("N,K,group,zero,M", [(4100, 256, 64, False, 40), (8300, 160, 32, True, 20), (4100, 384, 128, True, 90),
+                                              (2000, 256, 32, True, 530), (1000, 224, 32, False, 1101)])
+def test_many_tokens(N, K, group, zero, M):
+    """Two to four bands a workgroup for blocks of 32 tokens, and many rounds."""
+    q, scale, z = _weight(N, K, group, zero, torch.float16)
+    w = patch.w4_pack(q, scale, z, group)
+    x = torch.randn(M, K, generator=torch.Generator().manual_seed(M)).to(torch.float16).cuda()
+    for od in (None, torch.float32):
+        _check(x, q, scale, z, group, patch.w4_gemm(x, w, out_dtype=od), f"{od}")
+
+
+def test_more_tokens_than_a_launch_has():
+    q, scale, z = _weight(20, 32, 32, True, torch.bfloat16)
+    w = patch.w4_pack(q, scale, z, 32)
+    x = torch.randn(64, 32, generator=torch.Generator().manual_seed(1)).to(torch.bfloat16).cuda()
+    want = patch.w4_gemm(x, w)
+    y = patch.w4_gemm(x.repeat(32768, 1), w)  # 2^21 rows
+    assert torch.equal(y.view(32768, 64, 20), want.expand(32768, 64, 20))
+
+
 def test_packed_bytes_are_as_stated():
     """The layout of patch_w4_pack, byte by byte, and its padding."""
     N, K, group = 20, 160, 32
