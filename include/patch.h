@@ -570,7 +570,7 @@ patch_status patch_kv_append(const patch_kv_append_args* args, const patch_kv_ca
  * beyond max_pages * page: out and lse NaN.  Keys, values and scales that a
  * token does not see do not reach its output, NaN among them.  Scales must
  * be finite and not negative.  Rows of out and lse behind cu_new[S] are left
- * as they are.
+ * as they are.  out may be q, with its strides and type.
  *   workspace: patch_attention_workspace_bytes(...) bytes of scratch, 16-byte
  * aligned, contents of no matter before and after; calls that may run at the
  * same time need workspaces of their own.  NULL or a smaller one: no work is

@@ -229,6 +229,19 @@ def test_graph_of_chunks_follows_lengths():
         assert torch.equal(out, patch.attention(c.q, c.cache, pt, lens, cu)), by
 
 
+@pytest.mark.parametrize("new,total", [([1, 1, 3], [9000, 40, 700]), ([130, 260], [2000, 260]), ([1, 0], [1, 5])])
+def test_in_place(new, total):
+    c = Case(new, total, 8, 2, 128, 64, "bf16")
+    want = c.run(check=False)[0]
+    for workspace in ("auto", None):
+        q = c.q.clone()
+        out = patch.attention(q, c.cache, c.pt.cuda(), c.lens.cuda(), c.cu.cuda(), out=q, workspace=workspace)
+        assert out is q and (workspace is None or torch.equal(q, want))
+    n = int(c.cu[-1])
+    wantd, _, size, ds = (t[:n] for t in c.want(128 ** -0.5, 0))
+    ref.assert_within(q[:n], wantd, ref.attention_bound(wantd, size, ds, int(c.lens.max()), q.dtype), "in place")
+
+
 def test_offsets_beyond_32_bits():
     """Pages whose bytes lie behind the first 4 GiB of a cache, appended to and
     attended to by one token and by a chunk."""
