@@ -17,8 +17,8 @@
 // Bound by HBM for prompts and by latency for a token a sequence, where a
 // block has a single row: there 8 lanes own a block and a wave 8 heads.  Heads
 // of 128, GPU time: a token to each of 64 sequences, 32 heads, in 5 us; 8
-// prompts of 500 to 2100 tokens, 8 cache and 32 query heads, 191 MB in 51 us
-// (3.7 TB/s; a copy of 1 GiB reaches 5.1).
+// prompts of 500 to 2100 tokens, 8 cache and 32 query heads, 191 MB in 46.9
+// us (4.1 TB/s; a copy of 1 GiB reaches 5.1).
 #include <algorithm>
 
 #include "rotate.h"
@@ -95,15 +95,20 @@ __device__ __forceinline__ float group_max(float x, float* lds) {
 // GW lanes a block, KEEP items of a lane held in registers.
 template <typename T, int V, int GW, int KEEP>
 __global__ __launch_bounds__(kThreads) void k_kv_append(patch_kv_append_args a, patch_kv_cache c, uint32_t kv_blocks,
-                                                        int q_tokens) {
+                                                        uint32_t q_share, int q_tokens) {
   __shared__ float lds[kThreads / 64];
   const int rot = (int)a.rot, D = (int)c.dim, items = D / (2 * V), B = (int)c.page;
   const bool inter = a.layout == PATCH_ROPE_INTERLEAVED;
   const int S = (int)a.S;
   const int32_t* cu = a.cu_new_dev;
 
-  if (blockIdx.x >= kv_blocks) {  // q of q_tokens tokens
-    const int ta = (int)(blockIdx.x - kv_blocks) * q_tokens, tb = min(ta + q_tokens, (int)a.T);
+  uint32_t q_before = __umulhi(blockIdx.x, q_share), q_upto = __umulhi(blockIdx.x + 1, q_share);
+  if (blockIdx.x - q_before >= kv_blocks) {
+    q_before = blockIdx.x - kv_blocks;
+    q_upto = q_before + 1;
+  }
+  if (q_upto > q_before) {  // q of q_tokens tokens
+    const int ta = (int)q_before * q_tokens, tb = min(ta + q_tokens, (int)a.T);
     int s = find_last(S, [&](int i) { return cu[i] <= ta; });
     const int per = kThreads / items;  // heads at a time (items <= 128)
     const int ci = (int)threadIdx.x % items;
@@ -131,13 +136,14 @@ __global__ __launch_bounds__(kThreads) void k_kv_append(patch_kv_append_args a, 
   constexpr int kGroups = GW < 64 ? 64 / GW : 1;  // groups of a wave, all of one unit
   const int lane = (int)threadIdx.x % GW;
   const int kinds = 2 * (int)c.kv_heads;
+  const uint32_t kv_block = blockIdx.x - q_before;
   int64_t unit;
   int kind;
   if constexpr (GW > 64) {
-    unit = blockIdx.x / (uint32_t)kinds;
-    kind = (int)(blockIdx.x % (uint32_t)kinds);
+    unit = kv_block / (uint32_t)kinds;
+    kind = (int)(kv_block % (uint32_t)kinds);
   } else {
-    const uint32_t wave = blockIdx.x * (kThreads / 64) + threadIdx.x / 64, per = (uint32_t)(kinds + kGroups - 1) / kGroups;
+    const uint32_t wave = kv_block * (kThreads / 64) + threadIdx.x / 64, per = (uint32_t)(kinds + kGroups - 1) / kGroups;
     unit = wave / per;
     kind = (int)(wave % per) * kGroups + (int)(threadIdx.x & 63) / GW;
   }
@@ -248,10 +254,16 @@ hipError_t go(const patch_kv_append_args& a, const patch_kv_cache& c, hipStream_
   // query heads: 1024 tokens 8.1 us to 8.6, 2048 tokens 12.7 to 11.8, 16384
   // tokens 89 to 86.
   const int q_tokens = a.T >= 2048 ? 2 : 1;
-  const int64_t all = blocks + (a.q_dev ? (a.T + q_tokens - 1) / q_tokens : 0);
+  const int64_t qs = a.q_dev ? (a.T + q_tokens - 1) / q_tokens : 0, all = blocks + qs;
   if (all > 0x7fffffff) return hipErrorInvalidValue;
+  // From 4096 tokens on three quarters of q's workgroups lie evenly among the
+  // others, whose waits they fill (before workgroup i lie i q_share / 2^32 of
+  // them); the rest, and all of fewer tokens, follow.  8 prompts as above 46.9
+  // us against 48.4, 8 of 1024 tokens 36.1 to 36.8; of 128 tokens 8.9 to 8.2.
+  const uint64_t mixed = a.T >= 4096 ? (uint64_t)qs * 3 / 4 : 0, first = (uint64_t)blocks + mixed;
+  const uint32_t q_share = (uint32_t)((mixed * 0x100000000ull + first - 1) / first);
   hipLaunchKernelGGL((k_kv_append<T, V, GW, KEEP>), dim3((unsigned)all), dim3(kThreads), 0, s, a, c, (uint32_t)blocks,
-                     q_tokens);
+                     q_share, q_tokens);
   return hipGetLastError();
 }
 

@@ -78,6 +78,15 @@ def test_append(new, past, heads, kv_heads, D, page, rot, layout, dtype):
     c.check(c.run(table, layout), table, layout)
 
 
+@pytest.mark.parametrize("new,past,heads,kv_heads,D,page,rows", [
+    ([2050], [3], 2, 1, 32, 64, 0), ([4099], [30], 2, 1, 32, 16, 7), ([1900, 0, 2300, 61], [0, 9, 100, 15], 6, 2, 48, 128, 0)])
+def test_many_tokens(new, past, heads, kv_heads, D, page, rows):
+    """q's workgroups of two tokens, behind the others and among them."""
+    c = Case(new, past, heads, kv_heads, D, page, torch.bfloat16, extra_rows=rows)
+    table = patch.rope_table(max(c.total), 32)
+    c.check(c.run(table), table)
+
+
 def test_token_by_token_through_pages():
     """Twenty steps of one token a sequence over two page borders: scales that
     grow take the earlier tokens with them."""
