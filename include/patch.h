@@ -563,7 +563,7 @@ patch_status patch_kv_append(const patch_kv_append_args* args, const patch_kv_ca
  * or PATCH_F32); lse (may be NULL): float32 [T][heads], the natural logarithm
  * of the softmax's sum.  Products run on the 16-bit matrix instructions (8-bit
  * values are exact in them), the probabilities rounded to 11 bits for the
- * second product; scores, maxima, sums and outputs are fp32, the outputs
+ * second product, to 22 where out is PATCH_F32; scores, maxima, sums and outputs are fp32, the outputs
  * rounded once.
  *   A token that sees no key (negative position): out 0, lse -infinity.  A
  * page number outside 0 .. pages - 1 among the pages it sees, or a length

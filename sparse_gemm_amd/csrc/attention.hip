@@ -28,7 +28,8 @@
 // % 16) * DP / 16 + j.
 //
 // 8-bit values become 16-bit ones exactly (q's type for the scores; fp16 for
-// the second product, whose probabilities keep 11 bits).  A block's
+// the second product, whose probabilities keep 11 bits, or 22 in two values and
+// products where the output is fp32).  A block's
 // k scale multiplies the scores, its v scale the probabilities, relative to
 // the largest v scale so far (vref), o being kept in units of it.
 //
@@ -166,7 +167,7 @@ __device__ __forceinline__ void start_rows(const Args& a, const Seq& sq, const T
   x.vref = 0.f;
 }
 
-template <bool BF16, int DP, int R>
+template <bool BF16, int DP, int R, bool WIDE>
 __device__ __forceinline__ void do_step(const Args& a, const Task& task, int step, Bytes<DP>& b,
                                         Rows<BF16, DP, R>& x) {
   constexpr int VB = Bytes<DP>::VB;
@@ -226,7 +227,7 @@ __device__ __forceinline__ void do_step(const Args& a, const Task& task, int ste
   }
   const float inv = x.vref > 0.f ? 1.0f / x.vref : 0.f;
   const float vf[2] = {b.vs[0] * inv, b.vs[1] * inv};
-  u32x4 pr[R];
+  u32x4 pr[R], rest[WIDE ? R : 1];
 #pragma unroll
   for (int r = 0; r < R; r++) {
     float p[8];
@@ -253,14 +254,16 @@ __device__ __forceinline__ void do_step(const Args& a, const Task& task, int ste
     }
     const float off = finite_or_0(x.m[r]) - kBias;
     float sum = 0.f;
-    f16x8 ph;
+    f16x8 ph, pl;
 #pragma unroll
     for (int i = 0; i < 8; i++) {
       const float e = exp2_(p[i] - off);
       sum += e;
       ph[i] = (_Float16)(e * vf[i >> 2]);
+      if constexpr (WIDE) pl[i] = (_Float16)(e * vf[i >> 2] - (float)ph[i]);
     }
     pr[r] = __builtin_bit_cast(u32x4, ph);
+    if constexpr (WIDE) rest[r] = __builtin_bit_cast(u32x4, pl);
     x.l[r] += sum;
   }
 
@@ -274,7 +277,10 @@ __device__ __forceinline__ void do_step(const Args& a, const Task& task, int ste
 #pragma unroll
     for (int j = 0; j < 4; j++)
 #pragma unroll
-      for (int r = 0; r < R; r++) x.o[r][4 * w + j] = mma_dense<false>(e[j], pr[r], x.o[r][4 * w + j]);
+      for (int r = 0; r < R; r++) {
+        x.o[r][4 * w + j] = mma_dense<false>(e[j], pr[r], x.o[r][4 * w + j]);
+        if constexpr (WIDE) x.o[r][4 * w + j] = mma_dense<false>(e[j], rest[r], x.o[r][4 * w + j]);
+      }
   }
   if (nan_v) {
     // rare: V holds NaN in a row that not every row of the task sees.  A sum of
@@ -316,7 +322,8 @@ __device__ __forceinline__ void do_step(const Args& a, const Task& task, int ste
   }
 }
 
-template <bool BF16, int DP, int R>
+// WIDE: the probabilities in two fp16 values, 22 bits, for fp32 outputs.
+template <bool BF16, int DP, int R, bool WIDE = false>
 struct Few {
   static constexpr bool kBf16 = BF16;
   static constexpr int kWaves = patch::kWaves, kDim = DP, kRows = 16 * R, kStep = patch::kStep;
@@ -345,7 +352,7 @@ struct Few {
         if ((i & 63) == 0) pages = load_pages(a, table, h, step + kWaves, task.last_pos);
         next = load_step<DP>(a, pages, i & 63, h, step + kWaves, task.last_pos);
       }
-      do_step<BF16, DP, R>(a, task, step, cur, x);
+      do_step<BF16, DP, R, WIDE>(a, task, step, cur, x);
       cur = next;
     }
   } else {
@@ -423,13 +430,15 @@ bool many_rows(int64_t T, int64_t S, int64_t group, int64_t dim) { return dim <=
 // to 29.6, 64 rows 56 to 41.
 int tile_rows(int64_t T, int64_t S, int64_t group, int64_t dim) { return T * group <= 16 * S || dim > 128 ? 1 : 2; }
 
-template <bool BF16>
+template <bool BF16, bool WIDE>
 hipError_t by_shape(Args& a, void* ws, uint64_t ws_bytes, hipStream_t s) {
   if (many_rows(a.T, a.S, a.group, a.D)) return launch_attention_chunk(BF16, a, ws, ws_bytes, s);
   const int R = tile_rows(a.T, a.S, a.group, a.D);
-  if (a.D <= 64) return R == 1 ? go<Few<BF16, 64, 1>>(a, ws, ws_bytes, s) : go<Few<BF16, 64, 2>>(a, ws, ws_bytes, s);
-  if (a.D <= 128) return R == 1 ? go<Few<BF16, 128, 1>>(a, ws, ws_bytes, s) : go<Few<BF16, 128, 2>>(a, ws, ws_bytes, s);
-  return go<Few<BF16, 256, 1>>(a, ws, ws_bytes, s);
+  if (a.D <= 64)
+    return R == 1 ? go<Few<BF16, 64, 1, WIDE>>(a, ws, ws_bytes, s) : go<Few<BF16, 64, 2, WIDE>>(a, ws, ws_bytes, s);
+  if (a.D <= 128)
+    return R == 1 ? go<Few<BF16, 128, 1, WIDE>>(a, ws, ws_bytes, s) : go<Few<BF16, 128, 2, WIDE>>(a, ws, ws_bytes, s);
+  return go<Few<BF16, 256, 1, WIDE>>(a, ws, ws_bytes, s);
 }
 
 }  // namespace
@@ -501,7 +510,9 @@ hipError_t launch_attention(const patch_attention_args& p, const patch_kv_cache&
   a.q_wide = ((p.q_token | p.q_head) & 7) == 0 && ((uintptr_t)p.q_dev & 15) == 0;
   a.o_wide = ((p.out_token | p.out_head) & 7) == 0 && ((uintptr_t)p.out_dev & 15) == 0;
   a.out_f32 = p.out_dtype == PATCH_F32;
-  return p.dtype == PATCH_BF16 ? by_shape<true>(a, ws, ws_bytes, s) : by_shape<false>(a, ws, ws_bytes, s);
+  if (a.out_f32)
+    return p.dtype == PATCH_BF16 ? by_shape<true, true>(a, ws, ws_bytes, s) : by_shape<false, true>(a, ws, ws_bytes, s);
+  return p.dtype == PATCH_BF16 ? by_shape<true, false>(a, ws, ws_bytes, s) : by_shape<false, false>(a, ws, ws_bytes, s);
 }
 
 }  // namespace patch

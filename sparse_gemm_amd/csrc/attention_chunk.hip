@@ -36,8 +36,9 @@ constexpr int kSubs = kTile / 16;    // its sub-tiles of 16 keys, each in one pa
 // Waits for this wave's LDS traffic, not for loads from memory, and meets the others.
 __device__ __forceinline__ void meet() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
-// FULL: dim is DP, and a row's distance a constant.
-template <bool BF16, int DP, int R, bool FULL>
+// FULL: dim is DP, and a row's distance a constant.  WIDE: the probabilities in
+// two fp16 values, 22 bits, for fp32 outputs.
+template <bool BF16, int DP, int R, bool FULL, bool WIDE = false>
 struct Chunk {
   static constexpr bool kBf16 = BF16;
   static constexpr int kWaves = 8, kDim = DP, kRows = kWaves * 16 * R, kStep = kTile;
@@ -311,11 +312,11 @@ struct Chunk {
         // probabilities times the v scale (relative to vref): 2^(s + log2(vs) - m
         // + kBias), one multiply-add and the exponential; the sum takes them
         // divided by it again
-        u32x4 pr[R];
+        u32x4 pr[R], rest[WIDE ? R : 1];
 #pragma unroll
         for (int r = 0; r < R; r++) {
           const float mu = finite_or_0(m[r]);
-          f16x8 ph;
+          f16x8 ph, pl;
 #pragma unroll
           for (int t = 0; t < 2; t++) {
             const float off = lv[t] - mu;
@@ -325,17 +326,22 @@ struct Chunk {
               const float e = exp2_(fmaf(cur[r][t][i], ks[t], off));
               sum += e;
               ph[4 * t + i] = (_Float16)e;
+              if constexpr (WIDE) pl[4 * t + i] = (_Float16)(e - (float)ph[4 * t + i]);
             }
             l[r] = fmaf(sum, vi[t], l[r]);
           }
           pr[r] = __builtin_bit_cast(u32x4, ph);
+          if constexpr (WIDE) rest[r] = __builtin_bit_cast(u32x4, pl);
         }
         const u32x4* vf = frags + (st * 2 + 1) * kFrags * 64 + lane;
 #pragma unroll
         for (int j = 0; j < DP / 16; j++) {
           const u32x4 v = vf[j * 64];
 #pragma unroll
-          for (int r = 0; r < R; r++) o[r][j] = mma_dense<false>(v, pr[r], o[r][j]);
+          for (int r = 0; r < R; r++) {
+            o[r][j] = mma_dense<false>(v, pr[r], o[r][j]);
+            if constexpr (WIDE) o[r][j] = mma_dense<false>(v, rest[r], o[r][j]);
+          }
         }
       }
       if (nan_v) {
@@ -442,6 +448,14 @@ hipError_t by_rows(Args& a, void* ws, uint64_t ws_bytes, hipStream_t s) {
   return wave_rows(a.T, a.S, a.group) == 1 ? by_dim<BF16, 1>(a, ws, ws_bytes, s) : by_dim<BF16, 2>(a, ws, ws_bytes, s);
 }
 
+// fp32 outputs: 16 rows a wave, whose registers hold the second half of the
+// probabilities as well (a workspace for 32 is large enough).
+template <bool BF16>
+hipError_t wide(Args& a, void* ws, uint64_t ws_bytes, hipStream_t s) {
+  return a.D <= 64 ? go<Chunk<BF16, 64, 1, false, true>>(a, ws, ws_bytes, s)
+                   : go<Chunk<BF16, 128, 1, false, true>>(a, ws, ws_bytes, s);
+}
+
 }  // namespace
 
 uint64_t attention_chunk_workspace_bytes(int64_t T, int64_t S, int64_t group, int64_t dim) {
@@ -451,6 +465,7 @@ uint64_t attention_chunk_workspace_bytes(int64_t T, int64_t S, int64_t group, in
 }
 
 hipError_t launch_attention_chunk(bool bf16, Args& a, void* ws, uint64_t ws_bytes, hipStream_t s) {
+  if (a.out_f32) return bf16 ? wide<true>(a, ws, ws_bytes, s) : wide<false>(a, ws, ws_bytes, s);
   return bf16 ? by_rows<true>(a, ws, ws_bytes, s) : by_rows<false>(a, ws, ws_bytes, s);
 }
 

@@ -90,6 +90,23 @@ def test_attention(new, total, heads, kv_heads, D, page, window, dtype, out, wor
     Case(new, total, heads, kv_heads, D, page, dtype).run(window, TYPES[out], workspace=workspace)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("new,total,heads,kv_heads,D,window", [
+    ([1, 1], [700, 40], 4, 4, 128, 0), ([5, 1], [90, 300], 8, 2, 80, 0), ([9], [1000], 8, 2, 64, 100),
+    ([3], [200], 2, 1, 256, 0), ([90, 70], [400, 70], 4, 2, 128, 0), ([130], [500], 2, 1, 48, 200)])
+def test_float32_outputs_keep_22_bits(new, total, heads, kv_heads, D, window, dtype):
+    """Probabilities are 2^6 at the largest and held as two fp16 values: 2^-22
+    of each, and 2^-25 (the second's least step) of each of the n keys' |v| <=
+    448 v_scale, over a sum of 2^6 or more."""
+    c = Case(new, total, heads, kv_heads, D, 32, dtype)
+    c.cache.v_scale.fill_(2.0 ** -6)
+    out, _ = c.run(window, torch.float32)
+    want, _, size, ds = c.want(D ** -0.5, window)
+    n = max(total)
+    err = size * (2.0 ** -21 + 2 * ds[..., None] + (2 * n + 32) * ref.U32) + n * 2.0 ** -31 * 448 * 2.0 ** -6
+    ref.assert_within(out, want, ref.rounded(want, torch.float32, err), "out")
+
+
 def test_long_cache():
     Case([1, 1], [20011, 7], 2, 1, 128, 64, "f16").run()
 
